@@ -207,7 +207,9 @@ int enqueue_decode(const pa_dims* d, const Plan& plan, const void* q, const void
   p.kv_dtype = kv_dtype;
   p.group = d->num_q_heads / d->num_kv_heads;
   p.rows = n_query * p.group;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // The kernels take the first reference maximum through scale * -inf, which
+  // must be -inf: a scale of 0 becomes one that leaves every weight 1.
+  p.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;
   p.halves = plan.halves;
   p.rows_half = plan.rows_half;
   p.mode = plan.mode;
