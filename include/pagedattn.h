@@ -96,7 +96,9 @@ typedef enum {
   PA_ERR_CUDA = -4,           /* a CUDA runtime call or launch failed */
   PA_ERR_BAD_BLOCK_INDEX = -5,/* device saw block_table entry out of range */
   PA_ERR_BAD_CONTEXT_LEN = -6,/* device saw context_lens out of range */
-  PA_ERR_TIMEOUT = -7         /* a device-side wait gave up (kernel left early) */
+  PA_ERR_TIMEOUT = -7,        /* a device-side wait gave up (kernel left early) */
+  PA_ERR_BAD_REQUEST = -8,    /* device refused a page operation's request */
+  PA_ERR_NO_PAGES = -9        /* device found too few free pages */
 } pa_status;
 
 /* Static shapes of one call.  Host memory, read during the call only. */
@@ -165,6 +167,37 @@ int paged_attn_decode_partial(const pa_dims* dims, const void* q, const void* k_
                               int32_t window, float scale, int32_t kv_dtype, float* out,
                               float* out_lse, void* stream);
 
+/* Decode attention for a batch whose sequences share a long prefix, read and
+ * scored once for all of them.  The same computation as paged_attn_decode
+ * for sequences whose first P = *prefix_len keys (device int32 [1]) are the
+ * same: those keys are read through prefix_table (device int32
+ * [prefix_blocks], the physical blocks of keys 0, block_size, ...), the keys
+ * [P, L_s) through row s of the ordinary block_table, whose first
+ * P / block_size entries are not read.  A row of block_table may serve as
+ * the prefix_table.  context_lens, positions, masks and the window are those
+ * of the whole sequence; new tokens may lie inside the prefix.  P is 0 or a
+ * multiple of block_size, at most prefix_blocks * block_size and at most
+ * every L_s; the device checks it, and a P that is not gives rows of 0 and
+ * PA_ERR_BAD_CONTEXT_LEN (for a sequence shorter than P: its rows alone), a
+ * block out of range rows of 0 for the rows that see it and
+ * PA_ERR_BAD_BLOCK_INDEX.  Results need not be bit-identical to
+ * paged_attn_decode's (another order of the sums); repeated calls give
+ * bit-identical results, and a sequence's result does not depend on the
+ * values of the others.  The workspace must have
+ * paged_attn_shared_workspace_size bytes, be initialised by
+ * paged_attn_workspace_init and may serve paged_attn_decode calls too. */
+int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_cache,
+                             const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, const int32_t* prefix_table,
+                             const int32_t* prefix_len, int32_t prefix_blocks, int32_t n_query,
+                             int32_t causal, int32_t window, float scale, int32_t kv_dtype,
+                             void* out, void* stream);
+
+/* Bytes of workspace paged_attn_decode_shared needs, any cache type, any
+ * device.  Host only.  Returns 0 for invalid shapes. */
+size_t paged_attn_shared_workspace_size(const pa_dims* dims, int32_t n_query,
+                                        int32_t prefix_blocks);
+
 /* Log-sum-exp merge of split partials ("Dual MI50, part 2", section
  * "Decode: a new kernel for the shape MTP actually runs": partial results
  * are merged at the end).  For each row r:
@@ -182,9 +215,9 @@ int paged_attn_merge(const float* partial_out, const float* partial_lse,
                      void* out, float* out_lse, void* stream);
 
 /* Synchronises `stream`, then returns and clears the device-side data-error
- * flag of the workspace: PA_OK, PA_ERR_TIMEOUT, PA_ERR_BAD_BLOCK_INDEX or
- * PA_ERR_BAD_CONTEXT_LEN (the first of these that was raised, in that order),
- * or PA_ERR_CUDA if the stream reports an error.  PA_ERR_TIMEOUT means a
+ * flag of the workspace: PA_OK, PA_ERR_TIMEOUT, PA_ERR_BAD_BLOCK_INDEX,
+ * PA_ERR_BAD_CONTEXT_LEN, PA_ERR_BAD_REQUEST or PA_ERR_NO_PAGES (the first of
+ * these that was raised, in that order), or PA_ERR_CUDA if the stream reports an error.  PA_ERR_TIMEOUT means a
  * pipeline wait inside a kernel passed its time limit: the kernel released
  * its resources and returned and its output is not valid; the workspace
  * stays usable (this call also clears its counters, as a safety net). */
@@ -228,6 +261,78 @@ int paged_attn_cache_write(const pa_dims* dims, const void* k_new, const void* v
                            const int32_t* block_table, const int32_t* context_lens,
                            int32_t n_new, int32_t kv_dtype, void* k_cache, void* v_cache,
                            void* stream);
+
+/* ---- Page operations -----------------------------------------------------
+ * Sequences share physical blocks (pages): one prompt with several answers,
+ * a common system prompt.  The books are three device arrays that the
+ * caller owns, all read and written by these calls:
+ *   block_table   int32 [num_seqs][max_blocks_per_seq]; a row holds the
+ *                 first ceil(L / block_size) of its entries
+ *   context_lens  int32 [num_seqs]; 0 = an empty row
+ *   ref_counts    int32 [num_blocks]: how many rows hold a page; 0 = free
+ * Entries behind a row's last page are never read and left as they were.  A
+ * new pool has every length and count 0.  Fresh pages are the lowest free
+ * ones at the start of the call, handed out in the order of the requests:
+ * results are determined by the books and the requests.  Nothing is copied
+ * to the host; everything can be captured in a graph.  dims->workspace:
+ * paged_attn_pages_workspace_size bytes, initialised once by
+ * paged_attn_pages_workspace_init, not shared with attention calls or with
+ * another page operation that may overlap; paged_attn_get_error reports
+ * what the device refused.  A request that is refused leaves its row and
+ * pages as they were; the others are carried out. */
+size_t paged_attn_pages_workspace_size(const pa_dims* dims);
+int paged_attn_pages_workspace_init(const pa_dims* dims, void* stream);
+
+/* Fork: row children[i] (an empty row) becomes a copy of row parents[i] and
+ * holds the same pages, the ragged last one included (device int32 [n],
+ * n <= num_seqs).  No data moves.  Refused (PA_ERR_BAD_REQUEST): a row out
+ * of range, a child that is not empty or that an earlier request has, a
+ * parent that is a child of the same call. */
+int paged_attn_fork(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
+                    int32_t* ref_counts, const int32_t* parents, const int32_t* children,
+                    int32_t n, void* stream);
+
+/* Resize: row rows[i] gets the length new_lens[i] (device int32 [n], n <=
+ * num_seqs; new_lens NULL: 0 for all, which frees the rows).  A shorter row
+ * gives up the pages behind its new end (a page that no row holds any more
+ * is free from the next call on); a longer one gets fresh pages.  A row that
+ * grows out of a ragged last page that other rows hold too gets a fresh page
+ * for it, and copy_src[i], copy_dst[i] (device int32 [n], written for every
+ * request) ask for the copy: the caller runs paged_attn_copy_blocks with
+ * them on every layer's caches before it writes the new tokens.  When all
+ * holders of a ragged page grow in one call, the last of them keeps it.
+ * copy_src[i] = copy_dst[i] = -1 where nothing is to be copied.  Refused: a
+ * row out of range or named by an earlier request (PA_ERR_BAD_REQUEST), a
+ * length outside [0, max_blocks_per_seq * block_size]
+ * (PA_ERR_BAD_CONTEXT_LEN); from the first growing request on that the free
+ * pages do not suffice for, every growing request (PA_ERR_NO_PAGES). */
+int paged_attn_resize(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
+                      int32_t* ref_counts, const int32_t* rows, const int32_t* new_lens, int32_t n,
+                      int32_t* copy_src, int32_t* copy_dst, void* stream);
+
+/* Compact: with n_live live pages, the k-th lowest live page at or above
+ * n_live moves to the k-th lowest free page below it, so that the live pages
+ * are the first n_live.  Rewrites the tables and counts and writes the moves
+ * to copy_src, copy_dst (device int32 [max(1, num_blocks / 2)], -1 behind
+ * the last), their number to *count (device int32 [1]) and, for every page,
+ * where it went to remap (device int32 [num_blocks], -1: free), for lists of
+ * pages that the caller keeps elsewhere.  The caller runs
+ * paged_attn_copy_blocks with the moves on every layer's caches. */
+int paged_attn_compact(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
+                       int32_t* ref_counts, int32_t* copy_src, int32_t* copy_dst, int32_t* count,
+                       int32_t* remap, void* stream);
+
+/* Copies whole pages inside one layer's caches, K and V: page copy_dst[i]
+ * becomes a copy of page copy_src[i] for i < n (device int32 [n], n <=
+ * num_blocks), or i < min(n, *count) where count (device int32 [1]) is not
+ * NULL.  A negative copy_src[i] is skipped.  No page may be written twice or
+ * both read and written: of pairs with one target the lowest stands, a pair
+ * whose source is a target does not (PA_ERR_BAD_REQUEST), and a page out of
+ * range is not copied (PA_ERR_BAD_BLOCK_INDEX).  n and count apart, the
+ * books are not used. */
+int paged_attn_copy_blocks(const pa_dims* dims, const int32_t* copy_src, const int32_t* copy_dst,
+                           int32_t n, const int32_t* count, int32_t kv_dtype, void* k_cache,
+                           void* v_cache, void* stream);
 
 /* The most split partials one (sequence, KV head, row part) of a call with
  * these shapes and cache type is merged from on the current device (host

@@ -25,6 +25,8 @@ PA_ERR_CUDA = -4
 PA_ERR_BAD_BLOCK_INDEX = -5
 PA_ERR_BAD_CONTEXT_LEN = -6
 PA_ERR_TIMEOUT = -7
+PA_ERR_BAD_REQUEST = -8
+PA_ERR_NO_PAGES = -9
 
 KV_FP16 = _inputs.KV_FP16
 KV_Q8_0 = _inputs.KV_Q8_0
@@ -88,6 +90,23 @@ def lib() -> ctypes.CDLL:
             L.paged_attn_launches_per_call.restype = ctypes.c_int32
             L.paged_attn_status_string.argtypes = [i32]
             L.paged_attn_status_string.restype = ctypes.c_char_p
+            L.paged_attn_shared_workspace_size.argtypes = [P, i32, i32]
+            L.paged_attn_shared_workspace_size.restype = ctypes.c_size_t
+            L.paged_attn_decode_shared.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32,
+                                                   i32, f32, i32, vp, vp]
+            L.paged_attn_decode_shared.restype = ctypes.c_int
+            L.paged_attn_pages_workspace_size.argtypes = [P]
+            L.paged_attn_pages_workspace_size.restype = ctypes.c_size_t
+            L.paged_attn_pages_workspace_init.argtypes = [P, vp]
+            L.paged_attn_pages_workspace_init.restype = ctypes.c_int
+            L.paged_attn_fork.argtypes = [P, vp, vp, vp, vp, vp, i32, vp]
+            L.paged_attn_fork.restype = ctypes.c_int
+            L.paged_attn_resize.argtypes = [P, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+            L.paged_attn_resize.restype = ctypes.c_int
+            L.paged_attn_compact.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.paged_attn_compact.restype = ctypes.c_int
+            L.paged_attn_copy_blocks.argtypes = [P, vp, vp, i32, vp, i32, vp, vp, vp]
+            L.paged_attn_copy_blocks.restype = ctypes.c_int
             _LIB = L
         return _LIB
 

@@ -32,6 +32,77 @@ int prepare_decode(const pa_dims* dims, const void* q, const void* k_cache, cons
   if (dims->workspace_bytes < ws_layout(dims, n_query, *plan).total) return PA_ERR_WORKSPACE;
   return PA_OK;
 }
+
+// Workspace of a shared-prefix call: the decode layout (any device, so that
+// the offsets behind it are the same everywhere), the own-keys part, the
+// prefix partials.
+struct SharedWs {
+  size_t own_out, own_lse, part_out, part_lse, total;
+};
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+SharedWs shared_ws(const pa_dims* d, int n_query, const SharedPlan& pl) {
+  const size_t rows = (size_t)d->num_seqs * n_query * d->num_q_heads;
+  SharedWs w;
+  w.own_out = align256(ws_size_any_device(d, n_query));
+  w.own_lse = w.own_out + rows * kHeadDim * sizeof(float);
+  w.part_out = w.own_lse + align256(rows * sizeof(float));
+  w.part_lse = w.part_out + (size_t)pl.part_rows * kHeadDim * sizeof(float);
+  w.total = w.part_lse + align256((size_t)pl.part_rows * sizeof(float));
+  return w;
+}
+int check_shared(const pa_dims* d, int n_query, int prefix_blocks) {
+  const int rc = check_dims(d, n_query);
+  if (rc != PA_OK) return rc;
+  if (prefix_blocks < 1) return PA_ERR_INVALID_ARG;
+  if ((long long)prefix_blocks * d->block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// Workspace of the page operations: status header, per-request and per-page
+// scratch.
+struct PagesWs {
+  size_t rows, pages, small, total;
+};
+PagesWs pages_ws(const pa_dims* d) {
+  PagesWs w;
+  w.rows = kWsHeader;
+  w.pages = w.rows + align256((size_t)d->num_seqs * 3 * sizeof(int));
+  w.small = w.pages + align256((size_t)d->num_blocks * 3 * sizeof(int));
+  w.total = w.small + 256;
+  return w;
+}
+// The checks and parameters that the page operations have in common.
+int prepare_pages(const pa_dims* d, PageParams* p) {
+  const int rc = check_dims(d, 1);
+  if (rc != PA_OK) return rc;
+  const PagesWs w = pages_ws(d);
+  if (d->workspace == nullptr || !aligned(d->workspace, 256) || d->workspace_bytes < w.total)
+    return PA_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(d->workspace);
+  *p = PageParams{};
+  p->num_seqs = d->num_seqs;
+  p->max_blocks_per_seq = d->max_blocks_per_seq;
+  p->block_size = d->block_size;
+  p->num_blocks = d->num_blocks;
+  p->flags = reinterpret_cast<unsigned*>(ws);
+  p->row_scratch = reinterpret_cast<int*>(ws + w.rows);
+  p->page_scratch = reinterpret_cast<int*>(ws + w.pages);
+  p->small_scratch = reinterpret_cast<int*>(ws + w.small);
+  return PA_OK;
+}
+// The same with the books.
+int prepare_books(const pa_dims* d, int32_t* block_table, int32_t* context_lens,
+                  int32_t* ref_counts, PageParams* p) {
+  const int rc = prepare_pages(d, p);
+  if (rc != PA_OK) return rc;
+  if (!block_table || !context_lens || !ref_counts || !aligned(block_table, 4) ||
+      !aligned(context_lens, 4) || !aligned(ref_counts, 4))
+    return PA_ERR_INVALID_ARG;
+  p->block_table = block_table;
+  p->context_lens = context_lens;
+  p->ref_counts = ref_counts;
+  return PA_OK;
+}
 }  // namespace
 
 extern "C" {
@@ -116,6 +187,72 @@ int paged_attn_decode_partial(const pa_dims* dims, const void* q, const void* k_
                         static_cast<cudaStream_t>(stream), pa_args);
 }
 
+size_t paged_attn_shared_workspace_size(const pa_dims* dims, int32_t n_query,
+                                        int32_t prefix_blocks) {
+  if (check_shared(dims, n_query, prefix_blocks) != PA_OK) return 0;
+  return shared_ws(dims, n_query, make_shared_plan((long long)dims->num_seqs * n_query * dims->num_q_heads,
+                                            (long long)prefix_blocks * dims->block_size)).total;
+}
+
+int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_cache,
+                             const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, const int32_t* prefix_table,
+                             const int32_t* prefix_len, int32_t prefix_blocks, int32_t n_query,
+                             int32_t causal, int32_t window, float scale, int32_t kv_dtype,
+                             void* out, void* stream) {
+  int rc = check_shared(dims, n_query, prefix_blocks);
+  if (rc != PA_OK) return rc;
+  if (!prefix_table || !prefix_len || !aligned(prefix_table, 4) || !aligned(prefix_len, 4))
+    return PA_ERR_INVALID_ARG;
+  Plan plan;
+  rc = prepare_decode(dims, q, k_cache, v_cache, block_table, context_lens, n_query, causal, window,
+                      scale, kv_dtype, out, &plan);
+  if (rc != PA_OK) return rc;
+  const SharedPlan spl = make_shared_plan((long long)dims->num_seqs * n_query * dims->num_q_heads,
+                                            (long long)prefix_blocks * dims->block_size);
+  const SharedWs w = shared_ws(dims, n_query, spl);
+  if (dims->workspace_bytes < w.total) return PA_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(dims->workspace);
+  SharedParams p{};
+  p.q = static_cast<const __half*>(q);
+  p.k = k_cache;
+  p.v = v_cache;
+  p.prefix_table = prefix_table;
+  p.prefix_len = prefix_len;
+  p.context_lens = context_lens;
+  p.num_seqs = dims->num_seqs;
+  p.num_q_heads = dims->num_q_heads;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.block_size = dims->block_size;
+  p.max_blocks_per_seq = dims->max_blocks_per_seq;
+  p.num_blocks = dims->num_blocks;
+  p.n_query = n_query;
+  p.causal = causal;
+  p.window = window;
+  p.kv_dtype = kv_dtype;
+  p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.prefix_blocks = prefix_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.splits = spl.splits;
+  p.wait_limit_ns = wait_limit_ns();
+  p.own_out = reinterpret_cast<float*>(ws + w.own_out);
+  p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
+  p.part_out = reinterpret_cast<float*>(ws + w.part_out);
+  p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  p.flags = reinterpret_cast<unsigned*>(ws);
+  p.out = static_cast<__half*>(out);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (launch_prefix(p, st) != cudaSuccess) return PA_ERR_CUDA;
+  PartialArgs own;
+  own.prefix_len = prefix_len;
+  own.out = p.own_out;
+  own.out_lse = p.own_lse;
+  rc = enqueue_decode(dims, plan, q, k_cache, v_cache, block_table, context_lens, n_query, causal,
+                      window, scale, kv_dtype, nullptr, dims->workspace, nullptr, st, own);
+  if (rc != PA_OK) return rc;
+  return launch_shared_join(p, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 int paged_attn_trace(const pa_dims* dims, const void* q, const void* k_cache,
                      const void* v_cache, const int32_t* block_table,
                      const int32_t* context_lens, int32_t n_query, int32_t causal,
@@ -177,6 +314,8 @@ int paged_attn_get_error(const pa_dims* dims, void* stream) {
   if (flags & kFlagTimeout) return PA_ERR_TIMEOUT;
   if (flags & kFlagBadBlock) return PA_ERR_BAD_BLOCK_INDEX;
   if (flags & kFlagBadLen) return PA_ERR_BAD_CONTEXT_LEN;
+  if (flags & kFlagBadRequest) return PA_ERR_BAD_REQUEST;
+  if (flags & kFlagNoPages) return PA_ERR_NO_PAGES;
   return PA_OK;
 }
 
@@ -218,6 +357,105 @@ int paged_attn_cache_write(const pa_dims* dims, const void* k_new, const void* v
                                                                                  : PA_ERR_CUDA;
 }
 
+size_t paged_attn_pages_workspace_size(const pa_dims* dims) {
+  if (check_dims(dims, 1) != PA_OK) return 0;
+  return pages_ws(dims).total;
+}
+
+int paged_attn_pages_workspace_init(const pa_dims* dims, void* stream) {
+  const int rc = check_dims(dims, 1);
+  if (rc != PA_OK) return rc;
+  if (dims->workspace == nullptr || !aligned(dims->workspace, 256) ||
+      dims->workspace_bytes < pages_ws(dims).total)
+    return PA_ERR_WORKSPACE;
+  return cudaMemsetAsync(dims->workspace, 0, kWsHeader, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+int paged_attn_fork(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
+                    int32_t* ref_counts, const int32_t* parents, const int32_t* children,
+                    int32_t n, void* stream) {
+  PageParams p;
+  const int rc = prepare_books(dims, block_table, context_lens, ref_counts, &p);
+  if (rc != PA_OK) return rc;
+  if (n < 0 || n > dims->num_seqs) return PA_ERR_INVALID_ARG;
+  if (n == 0) return PA_OK;
+  if (!parents || !children || !aligned(parents, 4) || !aligned(children, 4))
+    return PA_ERR_INVALID_ARG;
+  p.parents = parents;
+  p.rows = children;
+  p.n = n;
+  return launch_fork(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int paged_attn_resize(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
+                      int32_t* ref_counts, const int32_t* rows, const int32_t* new_lens, int32_t n,
+                      int32_t* copy_src, int32_t* copy_dst, void* stream) {
+  PageParams p;
+  const int rc = prepare_books(dims, block_table, context_lens, ref_counts, &p);
+  if (rc != PA_OK) return rc;
+  if (n < 0 || n > dims->num_seqs) return PA_ERR_INVALID_ARG;
+  if (n == 0) return PA_OK;
+  if (!rows || !copy_src || !copy_dst || !aligned(rows, 4) || !aligned(copy_src, 4) ||
+      !aligned(copy_dst, 4) || (new_lens && !aligned(new_lens, 4)))
+    return PA_ERR_INVALID_ARG;
+  p.rows = rows;
+  p.new_lens = new_lens;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.n = n;
+  return launch_resize(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int paged_attn_compact(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
+                       int32_t* ref_counts, int32_t* copy_src, int32_t* copy_dst, int32_t* count,
+                       int32_t* remap, void* stream) {
+  PageParams p;
+  const int rc = prepare_books(dims, block_table, context_lens, ref_counts, &p);
+  if (rc != PA_OK) return rc;
+  if (!copy_src || !copy_dst || !count || !remap || !aligned(copy_src, 4) ||
+      !aligned(copy_dst, 4) || !aligned(count, 4) || !aligned(remap, 4))
+    return PA_ERR_INVALID_ARG;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.count = count;
+  p.remap = remap;
+  p.n = dims->num_blocks > 1 ? dims->num_blocks / 2 : 1;
+  return launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int paged_attn_copy_blocks(const pa_dims* dims, const int32_t* copy_src, const int32_t* copy_dst,
+                           int32_t n, const int32_t* count, int32_t kv_dtype, void* k_cache,
+                           void* v_cache, void* stream) {
+  PageParams p;
+  const int rc = prepare_pages(dims, &p);
+  if (rc != PA_OK) return rc;
+  if (n < 0 || n > dims->num_blocks) return PA_ERR_INVALID_ARG;
+  if (kv_dtype != PA_KV_FP16 && kv_dtype != PA_KV_Q8_0 && kv_dtype != PA_KV_INT8_ROW)
+    return PA_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return PA_ERR_INVALID_ARG;
+  if (n == 0) return PA_OK;
+  if (!copy_src || !copy_dst || !aligned(copy_src, 4) || !aligned(copy_dst, 4) ||
+      (count && !aligned(count, 4)))
+    return PA_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  p.copy_src = const_cast<int32_t*>(copy_src);
+  p.copy_dst = const_cast<int32_t*>(copy_dst);
+  p.count = const_cast<int32_t*>(count);
+  p.n = n;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.page_bytes = (long long)dims->num_kv_heads *
+                 (kv_dtype == PA_KV_FP16 ? (long long)dims->block_size * kHeadDim * 2
+                                         : quant_tile_bytes(kv_dtype, dims->block_size));
+  return launch_copy_blocks(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                      : PA_ERR_CUDA;
+}
+
 const char* paged_attn_status_string(int32_t status) {
   switch (status) {
     case PA_OK: return "ok";
@@ -228,6 +466,8 @@ const char* paged_attn_status_string(int32_t status) {
     case PA_ERR_BAD_BLOCK_INDEX: return "block_table entry out of range";
     case PA_ERR_BAD_CONTEXT_LEN: return "context length out of range";
     case PA_ERR_TIMEOUT: return "a device-side wait timed out; output invalid";
+    case PA_ERR_BAD_REQUEST: return "page request refused (repeated, occupied or out of range)";
+    case PA_ERR_NO_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }

@@ -26,7 +26,13 @@ constexpr int kMaxQueueSeqs = 256;
 constexpr unsigned long long kDefaultWaitLimitNs = 1000000000ull;  // 1 s
 
 // Device-side data-error flags (bits of the first uint32 of the workspace).
-enum : unsigned { kFlagBadBlock = 1u, kFlagBadLen = 2u, kFlagTimeout = 4u };
+enum : unsigned {
+  kFlagBadBlock = 1u,
+  kFlagBadLen = 2u,
+  kFlagTimeout = 4u,
+  kFlagBadRequest = 8u,  // a page operation's request was refused
+  kFlagNoPages = 16u     // the pool had too few free pages
+};
 
 enum KvDtype : int { kKvFp16 = 0, kKvQ8_0 = 1, kKvInt8Row = 2 };
 
@@ -95,6 +101,11 @@ struct DecodeParams {
   const int32_t* key_count;
   float* out_f32;
   float* out_lse;
+  // Own-keys mode (shared-prefix decode): the keys of every sequence are
+  // limited to [*prefix_len, L_s), found through its ordinary block_table
+  // row; fp32 outputs as in partial mode, with a NaN log-sum-exp for a row
+  // whose keys reach an out-of-range block.
+  const int32_t* prefix_len;  // null: no shared prefix
   int32_t* trace;             // null, or [B][nq][Hq][5] key-resolution record
   int coop;                   // every CTA of the grid is resident at once
 };

@@ -46,4 +46,60 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t stream);
 
+// Shared-prefix decode (shared_prefix.cu): the prefix part of every query
+// row, and its join with the own-keys part (launch_decode_tc in own-keys
+// mode).
+struct SharedPlan {
+  int splits;           // prefix partials per row
+  long long part_rows;  // rows of part_out
+};
+struct SharedParams {
+  const __half* q;              // [B][nq][Hq][D]
+  const void* k;                // cache, see pagedattn.h
+  const void* v;
+  const int32_t* prefix_table;  // [prefix_blocks]
+  const int32_t* prefix_len;    // [1]
+  const int32_t* context_lens;  // [B]
+  int num_seqs, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq;
+  int num_blocks, n_query, causal, window, kv_dtype, group, prefix_blocks;
+  float scale_log2;             // scale * log2(e)
+  int splits;
+  unsigned long long wait_limit_ns;
+  float* part_out;              // prefix partials [splits][rows][D]
+  float* part_lse;              // [splits][rows], natural log
+  float* own_out;               // own-keys part [rows][D]
+  float* own_lse;               // [rows], natural log
+  unsigned* flags;              // workspace status word
+  __half* out;                  // [B][nq][Hq][D]
+};
+SharedPlan make_shared_plan(long long rows, long long prefix_keys);
+cudaError_t launch_prefix(const SharedParams& p, cudaStream_t stream);
+cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
+
+// Page operations (pages.cu).
+struct PageParams {
+  int32_t* block_table;   // [num_seqs][max_blocks_per_seq]
+  int32_t* context_lens;  // [num_seqs]
+  int32_t* ref_counts;    // [num_blocks]: table rows that hold a page (0: free)
+  const int32_t* rows;    // requests: the row (fork: the child)
+  const int32_t* parents; // fork
+  const int32_t* new_lens;// resize; null: 0
+  int32_t* copy_src;      // copies asked for (copy: to make), -1: none
+  int32_t* copy_dst;
+  int32_t* count;         // compact: moves made; copy: pairs of the list, or null
+  int32_t* remap;         // compact: where every page went
+  void* k_cache;
+  void* v_cache;
+  long long page_bytes;   // of one cache
+  int num_seqs, max_blocks_per_seq, block_size, num_blocks, n;
+  unsigned* flags;        // workspace status word
+  int* row_scratch;       // [3][num_seqs]
+  int* page_scratch;      // [3][num_blocks]
+  int* small_scratch;     // [64]
+};
+cudaError_t launch_fork(const PageParams& p, cudaStream_t stream);
+cudaError_t launch_resize(const PageParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const PageParams& p, cudaStream_t stream);
+cudaError_t launch_copy_blocks(const PageParams& p, int sms, cudaStream_t stream);
+
 }  // namespace pa

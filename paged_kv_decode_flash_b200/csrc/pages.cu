@@ -1,0 +1,518 @@
+// pages.cu -- the page operations of a paged KV cache: sequences that share
+// pages (fork), grow, shrink and end (resize), a pool that is closed up
+// (compact), and the copies of whole pages that these ask for.
+//
+// The books are three device arrays: block_table, context_lens and
+// ref_counts[num_blocks], the number of table rows that hold a page (0: the
+// page is free).  There is no free list: the fresh pages of a call are the
+// lowest-numbered free ones, handed out in the order of the requests, so
+// every result follows from the books and the requests alone, whatever order
+// the threads run in (integer sums and minima commute; nothing else is
+// atomic).
+//
+// Bound: the bookkeeping calls move a few hundred kilobytes and are latency
+// (dependent trips to L2 between barriers); the copies are HBM bandwidth.
+// The planning kernels are one thread-block cluster, whose hardware barrier
+// joins the phases without a second launch.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace pa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kPlanCtas = 8;        // CTAs of a planning kernel (one cluster)
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanAll = kPlanCtas * kPlanThreads;
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster; what was written before is visible after.
+__device__ __forceinline__ void cluster_sync() {
+  __threadfence();
+  asm volatile(
+      "barrier.cluster.arrive.release;\n\t"
+      "barrier.cluster.wait.acquire;" ::
+          : "memory");
+}
+
+__device__ __forceinline__ bool page_ok(const PageParams& p, int page) {
+  return page >= 0 && page < p.num_blocks;
+}
+__device__ __forceinline__ bool row_ok(const PageParams& p, int row) {
+  return row >= 0 && row < p.num_seqs;
+}
+__device__ __forceinline__ bool len_ok(const PageParams& p, int len) {
+  return len >= 0 && (long long)len <= (long long)p.max_blocks_per_seq * p.block_size;
+}
+__device__ __forceinline__ int pages_of(const PageParams& p, int len) {
+  return (int)(((long long)len + p.block_size - 1) / p.block_size);
+}
+__device__ __forceinline__ int32_t* table_row(const PageParams& p, int row) {
+  return p.block_table + (long long)row * p.max_blocks_per_seq;
+}
+
+// Exclusive prefix sum over the CTA's threads, and the CTA's total.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // an earlier scan's sums have been read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    T s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  total = warp_sums[31];
+  return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// The pages of one CTA's share of the pool.
+__device__ __forceinline__ void pool_share(int num_blocks, int rank, int& b0, int& b1) {
+  b0 = (int)((long long)rank * num_blocks / kPlanCtas);
+  b1 = (int)((long long)(rank + 1) * num_blocks / kPlanCtas);
+}
+
+// ------------------------------------------------------------------- fork
+// One CTA per request.  A request stands unless a row is out of range, the
+// child has tokens, an earlier request has the same child, or the parent is
+// a child of the call itself (its row is being written).
+__global__ void __launch_bounds__(256) fork_kernel(const PageParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int par = __ldg(p.parents + i), child = __ldg(p.rows + i);
+  bool bad = !row_ok(p, par) || !row_ok(p, child);
+  for (int j = tid; j < p.n; j += blockDim.x) {
+    const int c = __ldg(p.rows + j);
+    bad |= c == par || (c == child && j < i);
+  }
+  int L = 0;
+  bool bad_len = false;
+  if (!bad) {
+    bad = __ldcg(p.context_lens + child) != 0;
+    L = __ldcg(p.context_lens + par);
+    bad_len = !len_ok(p, L);
+  }
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) atomicOr(p.flags, kFlagBadRequest);
+    return;
+  }
+  if (__syncthreads_or(bad_len)) {
+    if (tid == 0) atomicOr(p.flags, kFlagBadLen);
+    return;
+  }
+  const int held = pages_of(p, L);
+  const int32_t* from = table_row(p, par);
+  int32_t* to = table_row(p, child);
+  bool bad_page = false;
+  for (int b = tid; b < held; b += blockDim.x) bad_page |= !page_ok(p, __ldcg(from + b));
+  if (__syncthreads_or(bad_page)) {
+    if (tid == 0) atomicOr(p.flags, kFlagBadBlock);
+    return;
+  }
+  for (int b = tid; b < held; b += blockDim.x) {
+    const int page = __ldcg(from + b);
+    to[b] = page;
+    atomicAdd(p.ref_counts + page, 1);
+  }
+  if (tid == 0) p.context_lens[child] = L;
+}
+
+// ----------------------------------------------------------------- resize
+// Requests (row, new length).  Scratch: row_mark[row] the lowest request on
+// a row; holders[page] and keeper[page] how many requests grow out of the
+// ragged page and the last of them; need[i] / end[i] fresh pages of request
+// i and their running total; fresh[k] the k-th lowest free page.
+enum : int { kStands = 1, kGrows = 2, kSplits = 4 };
+
+__global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PageParams p) {
+  __shared__ int sums[32];
+  __shared__ long long long_sums[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rank = (int)cluster_rank(), tid = threadIdx.x;
+  const int gt = rank * kPlanThreads + tid;
+  int* row_mark = p.row_scratch;
+  int* need = p.row_scratch + p.num_seqs;
+  int* end = p.row_scratch + 2LL * p.num_seqs;
+  int* holders = p.page_scratch;
+  int* keeper = p.page_scratch + p.num_blocks;
+  int* fresh = p.page_scratch + 2LL * p.num_blocks;
+  int* share = p.small_scratch;  // [kPlanCtas] free pages of every CTA's share
+
+  // What request i asks for: its row, both lengths and, where it grows out
+  // of a ragged page, that page (-1: none).  0: it cannot stand on its own.
+  auto request = [&](int i, int& row, int& L, int& want, int& page) -> int {
+    row = __ldg(p.rows + i);
+    want = p.new_lens != nullptr ? __ldg(p.new_lens + i) : 0;
+    page = -1;
+    if (!row_ok(p, row)) {
+      atomicOr(p.flags, kFlagBadRequest);
+      return 0;
+    }
+    L = __ldcg(p.context_lens + row);
+    if (!len_ok(p, want) || !len_ok(p, L)) {
+      atomicOr(p.flags, kFlagBadLen);
+      return 0;
+    }
+    if (want > L && L % p.block_size != 0) {
+      page = __ldcg(table_row(p, row) + L / p.block_size);
+      if (!page_ok(p, page)) {
+        atomicOr(p.flags, kFlagBadBlock);
+        return 0;
+      }
+    }
+    return kStands | (want > L ? kGrows : 0);
+  };
+
+  for (int i = gt; i < p.n; i += kPlanAll) {
+    int row, L, want, page;
+    if (request(i, row, L, want, page) == 0) continue;
+    row_mark[row] = INT_MAX;
+    if (page >= 0) {
+      holders[page] = 0;
+      keeper[page] = -1;
+    }
+  }
+  cluster_sync();
+  for (int i = gt; i < p.n; i += kPlanAll) {
+    int row, L, want, page;
+    if (request(i, row, L, want, page) != 0) atomicMin(row_mark + row, i);
+  }
+  cluster_sync();
+  for (int i = gt; i < p.n; i += kPlanAll) {
+    int row, L, want, page;
+    if (request(i, row, L, want, page) == 0) continue;
+    if (__ldcg(row_mark + row) != i) {
+      atomicOr(p.flags, kFlagBadRequest);
+      continue;
+    }
+    if (page >= 0) {
+      atomicAdd(holders + page, 1);
+      atomicMax(keeper + page, i);
+    }
+  }
+  cluster_sync();
+  for (int i = gt; i < p.n; i += kPlanAll) {
+    int row, L, want, page, nd = 0;
+    const int st = request(i, row, L, want, page);
+    if ((st & kGrows) && __ldcg(row_mark + row) == i) {
+      nd = pages_of(p, want) - pages_of(p, L);
+      if (page >= 0) {
+        const int refs = __ldcg(p.ref_counts + page);
+        const bool keeps = __ldcg(holders + page) == refs && __ldcg(keeper + page) == i;
+        if (refs > 1 && !keeps) ++nd;
+      }
+    }
+    need[i] = nd;
+  }
+  int b0, b1, total;
+  pool_share(p.num_blocks, rank, b0, b1);
+  int mine = 0;
+  for (int b = b0 + tid; b < b1; b += kPlanThreads) mine += __ldcg(p.ref_counts + b) == 0;
+  block_scan(mine, sums, total);
+  if (tid == 0) share[rank] = total;
+  cluster_sync();
+  if (rank == 0) {
+    // 64 bits: many large requests may add up past the 32-bit range
+    long long run = 0, sum = 0;
+    for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
+      const int i = i0 + tid;
+      const long long nd = i < p.n ? __ldcg(need + i) : 0;
+      const long long e = run + block_scan(nd, long_sums, sum) + nd;
+      if (i < p.n) end[i] = (int)min(e, (long long)INT_MAX);
+      run += sum;
+    }
+    if (tid == 0) share[kPlanCtas] = (int)min(run, (long long)INT_MAX);
+  }
+  cluster_sync();
+  int base = 0, nfree = 0;
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int c = __ldcg(share + r);
+    if (r < rank) base += c;
+    nfree += c;
+  }
+  const int wanted = min(__ldcg(share + kPlanCtas), nfree);
+  for (int t0 = b0; t0 < b1 && base < wanted; t0 += kPlanThreads) {
+    const int b = t0 + tid;
+    const bool is_free = b < b1 && __ldcg(p.ref_counts + b) == 0;
+    const int k = base + block_scan((int)is_free, sums, total);
+    if (is_free && k < wanted) fresh[k] = b;
+    base += total;
+  }
+  cluster_sync();
+  // Carry out: one warp per request.
+  const int lane = tid % 32;
+  for (int i = gt / 32; i < p.n; i += kPlanAll / 32) {
+    // Lane 0 reads the request (it also writes the row's new length, last).
+    int row = 0, L = 0, want = 0, page = -1, st = 0;
+    if (lane == 0) {
+      row = __ldg(p.rows + i);
+      if (row_ok(p, row) && __ldcg(row_mark + row) == i) st = request(i, row, L, want, page);
+    }
+    st = __shfl_sync(0xffffffffu, st, 0);
+    row = __shfl_sync(0xffffffffu, row, 0);
+    L = __shfl_sync(0xffffffffu, L, 0);
+    want = __shfl_sync(0xffffffffu, want, 0);
+    page = __shfl_sync(0xffffffffu, page, 0);
+    const bool stands = st != 0;
+    int src = -1, dst = -1;
+    if (stands && (st & kGrows)) {
+      const int nd = __ldcg(need + i), e = __ldcg(end + i);
+      if (e > nfree) {
+        if (lane == 0) atomicOr(p.flags, kFlagNoPages);
+      } else {
+        const int have = pages_of(p, L), add = pages_of(p, want) - have;
+        const int32_t* f = fresh + (e - nd);
+        int32_t* t = table_row(p, row);
+        if (nd > add) {  // the ragged page is shared: its copy comes first
+          src = page;
+          dst = __ldcg(f);
+          ++f;
+          if (lane == 0) {
+            t[L / p.block_size] = dst;
+            atomicAdd(p.ref_counts + dst, 1);
+            atomicSub(p.ref_counts + page, 1);
+          }
+        }
+        for (int b = lane; b < add; b += 32) {
+          const int pg = __ldcg(f + b);
+          t[have + b] = pg;
+          atomicAdd(p.ref_counts + pg, 1);
+        }
+        if (lane == 0) p.context_lens[row] = want;
+      }
+    } else if (stands) {
+      const int32_t* t = table_row(p, row);
+      for (int b = pages_of(p, want) + lane; b < pages_of(p, L); b += 32) {
+        const int pg = __ldcg(t + b);
+        if (!page_ok(p, pg)) {
+          atomicOr(p.flags, kFlagBadBlock);
+        } else if (atomicSub(p.ref_counts + pg, 1) <= 0) {  // was not held: the books are wrong
+          atomicAdd(p.ref_counts + pg, 1);
+          atomicOr(p.flags, kFlagBadRequest);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) p.context_lens[row] = want;
+    }
+    if (lane == 0) {
+      p.copy_src[i] = src;
+      p.copy_dst[i] = dst;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- compact
+// n_live live pages; the k-th lowest live page at or above n_live moves to
+// the k-th lowest free page below it.
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const PageParams p) {
+  __shared__ int sums[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rank = (int)cluster_rank(), tid = threadIdx.x;
+  int* share = p.small_scratch;
+  int b0, b1, total, mine = 0;
+  pool_share(p.num_blocks, rank, b0, b1);
+  for (int b = b0 + tid; b < b1; b += kPlanThreads) mine += __ldcg(p.ref_counts + b) > 0;
+  block_scan(mine, sums, total);
+  if (tid == 0) share[rank] = total;
+  cluster_sync();
+  int before = 0, n_live = 0;
+  for (int r = 0; r < kPlanCtas; ++r) {
+    const int c = __ldcg(share + r);
+    if (r < rank) before += c;
+    n_live += c;
+  }
+  // Every page's rank among the live ones; gaps go into copy_dst by theirs.
+  // remap holds a high page's rank until its target is known.
+  if (n_live == p.num_blocks && rank == 0 && tid == 0) share[kPlanCtas] = 0;
+  for (int t0 = b0; t0 < b1; t0 += kPlanThreads) {
+    const int b = t0 + tid;
+    const bool live = b < b1 && __ldcg(p.ref_counts + b) > 0;
+    const int below = before + block_scan((int)live, sums, total);  // live pages below b
+    if (b < b1) {
+      p.remap[b] = !live ? -1 : b < n_live ? b : below;
+      if (!live && b < n_live) p.copy_dst[b - below] = b;
+      if (b == n_live) share[kPlanCtas] = n_live - below;  // live pages at or above n_live
+    }
+    before += total;
+  }
+  cluster_sync();
+  const int moves = __ldcg(share + kPlanCtas);
+  for (int b = max(b0, n_live) + tid; b < b1; b += kPlanThreads) {
+    const int below = p.remap[b];
+    if (below < 0) continue;
+    const int k = below - (n_live - moves);
+    const int to = __ldcg(p.copy_dst + k);
+    p.copy_src[k] = b;
+    p.remap[b] = to;
+    p.ref_counts[to] = p.ref_counts[b];
+    p.ref_counts[b] = 0;
+  }
+  for (int k = moves + rank * kPlanThreads + tid; k < p.n; k += kPlanAll) {
+    p.copy_src[k] = -1;
+    p.copy_dst[k] = -1;
+  }
+  if (rank == 0 && tid == 0) *p.count = moves;
+}
+
+// The tables after a compaction: one CTA per row.
+__global__ void __launch_bounds__(256) remap_kernel(const PageParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row = blockIdx.x;
+  const int L = __ldcg(p.context_lens + row);
+  if (!len_ok(p, L)) {
+    if (threadIdx.x == 0) atomicOr(p.flags, kFlagBadLen);
+    return;
+  }
+  const int held = pages_of(p, L);
+  int32_t* t = table_row(p, row);
+  for (int b = threadIdx.x; b < held; b += blockDim.x) {
+    const int page = __ldcg(t + b);
+    if (!page_ok(p, page)) {
+      atomicOr(p.flags, kFlagBadBlock);
+      continue;
+    }
+    const int to = __ldcg(p.remap + page);
+    if (to < 0) atomicOr(p.flags, kFlagBadRequest);  // the row holds a free page
+    else if (to != page) t[b] = to;
+  }
+}
+
+// ------------------------------------------------------------------- copy
+// Pairs (src, dst); a negative src is skipped.  A pair stands unless a page
+// is out of range, an earlier standing-range pair has the same target, or
+// its source is a target: then no page is written twice and none that is
+// read is written, whatever the order of the copies.  The list that stands
+// (-1 elsewhere) goes to scratch for copy_kernel.
+__global__ void __launch_bounds__(kPlanThreads, 1) copy_check_kernel(const PageParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int gt = (int)cluster_rank() * kPlanThreads + threadIdx.x;
+  int* owner = p.page_scratch;
+  int* src_ok = p.page_scratch + p.num_blocks;
+  const int n = p.count != nullptr ? max(0, min(p.n, __ldcg(p.count))) : p.n;
+  auto pair = [&](int i, int& s, int& d) -> bool {
+    s = __ldcg(p.copy_src + i);
+    d = __ldcg(p.copy_dst + i);
+    return s >= 0 && page_ok(p, s) && page_ok(p, d);
+  };
+  for (int i = gt; i < n; i += kPlanAll) {
+    int s, d;
+    if (pair(i, s, d)) {
+      owner[s] = INT_MAX;
+      owner[d] = INT_MAX;
+    } else if (s >= 0) {
+      atomicOr(p.flags, kFlagBadBlock);
+    }
+  }
+  cluster_sync();
+  for (int i = gt; i < n; i += kPlanAll) {
+    int s, d;
+    if (pair(i, s, d)) atomicMin(owner + d, i);
+  }
+  cluster_sync();
+  for (int i = gt; i < n; i += kPlanAll) {
+    int s, d;
+    bool ok = pair(i, s, d);
+    if (ok && (__ldcg(owner + d) != i || __ldcg(owner + s) != INT_MAX)) {
+      ok = false;
+      atomicOr(p.flags, kFlagBadRequest);
+    }
+    src_ok[i] = ok ? s : -1;
+  }
+}
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;                                  // 16-byte vectors per thread
+constexpr int kCopyPiece = kCopyThreads * kCopyVecs * 16;     // bytes per work unit
+
+// Persistent: units (pair, K or V, piece of a page) over the grid.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PageParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int* src_ok = p.page_scratch + p.num_blocks;
+  const int n = p.count != nullptr ? max(0, min(p.n, __ldcg(p.count))) : p.n;
+  const int pieces = (int)((p.page_bytes + kCopyPiece - 1) / kCopyPiece);
+  const long long units = (long long)n * 2 * pieces;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int i = (int)(u / (2 * pieces)), r = (int)(u % (2 * pieces));
+    const int s = __ldcg(src_ok + i);
+    if (s < 0) continue;
+    const int d = __ldcg(p.copy_dst + i);
+    uint8_t* base = static_cast<uint8_t*>(r < pieces ? p.k_cache : p.v_cache);
+    const long long off = (long long)(r % pieces) * kCopyPiece + threadIdx.x * 16;
+    const uint4* from = reinterpret_cast<const uint4*>(base + s * p.page_bytes + off);
+    uint4* to = reinterpret_cast<uint4*>(base + d * p.page_bytes + off);
+    uint4 x[kCopyVecs];
+#pragma unroll
+    for (int e = 0; e < kCopyVecs; ++e)
+      if (off + (long long)e * kCopyThreads * 16 < p.page_bytes) x[e] = __ldcs(from + e * kCopyThreads);
+#pragma unroll
+    for (int e = 0; e < kCopyVecs; ++e)
+      if (off + (long long)e * kCopyThreads * 16 < p.page_bytes) __stcs(to + e * kCopyThreads, x[e]);
+  }
+}
+
+cudaError_t launch(void (*kern)(const PageParams), unsigned grid, unsigned threads, int cluster,
+                   const PageParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const PageParams& p, cudaStream_t stream) {
+  return launch(fork_kernel, p.n, 256, 1, p, stream);
+}
+cudaError_t launch_resize(const PageParams& p, cudaStream_t stream) {
+  return launch(resize_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
+}
+cudaError_t launch_compact(const PageParams& p, cudaStream_t stream) {
+  const cudaError_t e = launch(compact_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
+  if (e != cudaSuccess) return e;
+  return launch(remap_kernel, p.num_seqs, 256, 1, p, stream);
+}
+cudaError_t launch_copy_blocks(const PageParams& p, int sms, cudaStream_t stream) {
+  const cudaError_t e = launch(copy_check_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)p.n * 2 * ((p.page_bytes + kCopyPiece - 1) / kCopyPiece);
+  const long long most = (long long)sms * 8;
+  return launch(copy_kernel, (unsigned)(units < most ? units : most), kCopyThreads, 1, p, stream);
+}
+
+}  // namespace pa

@@ -1,0 +1,81 @@
+"""Decode attention for a batch whose sequences share a long prefix.
+
+Argument marshalling for paged_attn_decode_shared (include/pagedattn.h): the
+prefix's keys are read and scored once for the query rows of all sequences,
+then joined with each sequence's own keys.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import binding as _b
+
+
+class SharedPrefixDecode(_b.PagedDecode):
+    """A PagedDecode configuration with room for a shared prefix of up to
+    ``prefix_blocks`` blocks.  The inherited calls (plain decode, partial,
+    cache_write, ...) work on the same workspace."""
+
+    def __init__(self, *, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                 block_size: int, max_blocks_per_seq: int, num_blocks: int, n_query: int,
+                 prefix_blocks: int, device=None, workspace=None):
+        d = _b.Dims(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                    max_blocks_per_seq, num_blocks, None, 0)
+        need = int(_b.lib().paged_attn_shared_workspace_size(ctypes.byref(d), n_query,
+                                                             int(prefix_blocks)))
+        if need == 0:
+            raise _b.PagedAttnError(_b.PA_ERR_INVALID_ARG, "shared_workspace_size (bad shapes)")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device or "cuda")
+        elif workspace.numel() * workspace.element_size() < need:
+            raise _b.PagedAttnError(_b.PA_ERR_WORKSPACE, "workspace too small")
+        with torch.cuda.device(workspace.device):
+            super().__init__(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
+                             head_dim=head_dim, block_size=block_size,
+                             max_blocks_per_seq=max_blocks_per_seq, num_blocks=num_blocks,
+                             n_query=n_query, workspace=workspace)
+        self.workspace_bytes = need
+        self.prefix_blocks = int(prefix_blocks)
+
+    @classmethod
+    def for_case(cls, case, prefix_blocks, device=None):
+        return cls(num_seqs=case.num_seqs, num_q_heads=case.num_q_heads,
+                   num_kv_heads=case.num_kv_heads, head_dim=case.head_dim,
+                   block_size=case.block_size, max_blocks_per_seq=case.max_blocks_per_seq,
+                   num_blocks=case.num_blocks, n_query=case.n_query, prefix_blocks=prefix_blocks,
+                   device=device)
+
+    def check_shared(self, prefix_table, prefix_len):
+        _b._expect(prefix_table, "prefix_table", torch.int32, (self.prefix_blocks,))
+        _b._expect(prefix_len, "prefix_len", torch.int32, (1,))
+        for name, t in (("prefix_table", prefix_table), ("prefix_len", prefix_len)):
+            if t.device != self.workspace.device:
+                raise ValueError(f"{name} is on {t.device}, the workspace on "
+                                 f"{self.workspace.device}")
+
+    def __call__(self, q, k_cache, v_cache, block_table, context_lens, prefix_table=None,
+                 prefix_len=None, *, causal: int, window: int, scale: float, kv_dtype: int,
+                 out=None, stream=None):
+        """paged_attn_decode_shared: the first prefix_len[0] keys of every
+        sequence are those of prefix_table (int32 [prefix_blocks]); without
+        both a plain decode."""
+        if prefix_table is None and prefix_len is None:
+            return super().__call__(q, k_cache, v_cache, block_table, context_lens, causal=causal,
+                                    window=window, scale=scale, kv_dtype=kv_dtype, out=out,
+                                    stream=stream)
+        self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
+        self.check_shared(prefix_table, prefix_len)
+        with torch.cuda.device(self.workspace.device):
+            if out is None:
+                out = torch.empty_like(q)
+                if stream is not None:
+                    out.record_stream(stream)
+            rc = _b.lib().paged_attn_decode_shared(
+                ctypes.byref(self.dims), _b._dptr(q), _b._dptr(k_cache), _b._dptr(v_cache),
+                _b._dptr(block_table), _b._dptr(context_lens), _b._dptr(prefix_table),
+                _b._dptr(prefix_len), self.prefix_blocks, self.n_query, int(causal), int(window),
+                float(scale), int(kv_dtype), _b._dptr(out), _b._stream_ptr(stream))
+        _b._check(rc, "paged_attn_decode_shared")
+        return out
