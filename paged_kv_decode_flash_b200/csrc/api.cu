@@ -37,17 +37,22 @@ int prepare_decode(const pa_dims* dims, const void* q, const void* k_cache, cons
 // the offsets behind it are the same everywhere), the own-keys part, the
 // prefix partials.
 struct SharedWs {
-  size_t own_out, own_lse, part_out, part_lse, total;
+  size_t own_out, own_lse, meta, part_lse, part_out, total;
 };
+SharedPlan shared_plan(const pa_dims* d, int n_query, int prefix_blocks, int kv_dtype, int sms) {
+  return make_shared_plan((long long)d->num_seqs * n_query * (d->num_q_heads / d->num_kv_heads),
+                          d->num_kv_heads, (long long)prefix_blocks * d->block_size, kv_dtype, sms);
+}
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 SharedWs shared_ws(const pa_dims* d, int n_query, const SharedPlan& pl) {
   const size_t rows = (size_t)d->num_seqs * n_query * d->num_q_heads;
   SharedWs w;
   w.own_out = align256(ws_size_any_device(d, n_query));
   w.own_lse = w.own_out + rows * kHeadDim * sizeof(float);
-  w.part_out = w.own_lse + align256(rows * sizeof(float));
-  w.part_lse = w.part_out + (size_t)pl.part_rows * kHeadDim * sizeof(float);
-  w.total = w.part_lse + align256((size_t)pl.part_rows * sizeof(float));
+  w.meta = w.own_lse + align256(rows * sizeof(float));
+  w.part_lse = w.meta + 256;
+  w.part_out = w.part_lse + align256((size_t)pl.part_rows * sizeof(float));
+  w.total = w.part_out + (size_t)pl.part_rows * kHeadDim * sizeof(float);
   return w;
 }
 int check_shared(const pa_dims* d, int n_query, int prefix_blocks) {
@@ -190,8 +195,11 @@ int paged_attn_decode_partial(const pa_dims* dims, const void* q, const void* k_
 size_t paged_attn_shared_workspace_size(const pa_dims* dims, int32_t n_query,
                                         int32_t prefix_blocks) {
   if (check_shared(dims, n_query, prefix_blocks) != PA_OK) return 0;
-  return shared_ws(dims, n_query, make_shared_plan((long long)dims->num_seqs * n_query * dims->num_q_heads,
-                                            (long long)prefix_blocks * dims->block_size)).total;
+  size_t need = 0;
+  for (int kv : {PA_KV_FP16, PA_KV_Q8_0})
+    need = std::max(need, shared_ws(dims, n_query, shared_plan(dims, n_query, prefix_blocks, kv,
+                                                               kMaxPrefixCtas)).total);
+  return need;
 }
 
 int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_cache,
@@ -208,8 +216,9 @@ int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_c
   rc = prepare_decode(dims, q, k_cache, v_cache, block_table, context_lens, n_query, causal, window,
                       scale, kv_dtype, out, &plan);
   if (rc != PA_OK) return rc;
-  const SharedPlan spl = make_shared_plan((long long)dims->num_seqs * n_query * dims->num_q_heads,
-                                            (long long)prefix_blocks * dims->block_size);
+  const int sms = device_sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  const SharedPlan spl = shared_plan(dims, n_query, prefix_blocks, kv_dtype, sms);
   const SharedWs w = shared_ws(dims, n_query, spl);
   if (dims->workspace_bytes < w.total) return PA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(dims->workspace);
@@ -232,17 +241,20 @@ int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_c
   p.kv_dtype = kv_dtype;
   p.group = dims->num_q_heads / dims->num_kv_heads;
   p.prefix_blocks = prefix_blocks;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.splits = spl.splits;
+  p.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;  // as in enqueue_decode
+  p.rows_head = spl.rows_head;
+  p.row_tile = spl.row_tile;
+  p.ctas = spl.ctas;
   p.wait_limit_ns = wait_limit_ns();
   p.own_out = reinterpret_cast<float*>(ws + w.own_out);
   p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
   p.part_out = reinterpret_cast<float*>(ws + w.part_out);
   p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  p.meta = reinterpret_cast<int*>(ws + w.meta);
   p.flags = reinterpret_cast<unsigned*>(ws);
   p.out = static_cast<__half*>(out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_prefix(p, st) != cudaSuccess) return PA_ERR_CUDA;
+  if (launch_prefix_tc(p, st) != cudaSuccess) return PA_ERR_CUDA;
   PartialArgs own;
   own.prefix_len = prefix_len;
   own.out = p.own_out;

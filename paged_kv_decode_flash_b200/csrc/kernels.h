@@ -46,11 +46,14 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t stream);
 
-// Shared-prefix decode (shared_prefix.cu): the prefix part of every query
-// row, and its join with the own-keys part (launch_decode_tc in own-keys
-// mode).
+// Shared-prefix decode: the prefix part of every query row (prefix_tc.cu) and
+// its join (shared_prefix.cu) with the own-keys part (launch_decode_tc in
+// own-keys mode).
+constexpr int kMaxPrefixCtas = 160;  // bound of the grid, whatever the device
 struct SharedPlan {
-  int splits;           // prefix partials per row
+  int rows_head;        // query rows of a KV head: sequences x tokens x group
+  int row_tile;         // of one CTA: 128 or 256
+  int ctas;
   long long part_rows;  // rows of part_out
 };
 struct SharedParams {
@@ -63,17 +66,26 @@ struct SharedParams {
   int num_seqs, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq;
   int num_blocks, n_query, causal, window, kv_dtype, group, prefix_blocks;
   float scale_log2;             // scale * log2(e)
-  int splits;
+  int rows_head, row_tile, ctas;// SharedPlan
   unsigned long long wait_limit_ns;
-  float* part_out;              // prefix partials [splits][rows][D]
-  float* part_lse;              // [splits][rows], natural log
+  float* part_out;              // prefix partials [slots][row_tile][D]
+  float* part_lse;              // [slots][row_tile], natural log
+  int* meta;                    // [2] key tiles of the prefix, CTAs that worked
   float* own_out;               // own-keys part [rows][D]
   float* own_lse;               // [rows], natural log
   unsigned* flags;              // workspace status word
   __half* out;                  // [B][nq][Hq][D]
 };
-SharedPlan make_shared_plan(long long rows, long long prefix_keys);
-cudaError_t launch_prefix(const SharedParams& p, cudaStream_t stream);
+// The shared prefix is whole blocks inside the caller's table.
+__host__ __device__ __forceinline__ bool shared_prefix_ok(const SharedParams& p, int P) {
+  return P >= 0 && P % p.block_size == 0 && P / p.block_size <= p.prefix_blocks;
+}
+__host__ __device__ __forceinline__ bool shared_seq_ok(const SharedParams& p, int L, int P) {
+  return context_len_ok(L, p.n_query, p.max_blocks_per_seq, p.block_size) && P <= L;
+}
+SharedPlan make_shared_plan(long long rows_head, int num_kv_heads, long long prefix_keys, int kv_dtype,
+                            int sms);
+cudaError_t launch_prefix_tc(const SharedParams& p, cudaStream_t stream);
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
 
 // Page operations (pages.cu).
