@@ -33,24 +33,22 @@ int prepare_decode(const pa_dims* dims, const void* q, const void* k_cache, cons
   return PA_OK;
 }
 
-// Workspace of a shared-prefix call: the decode layout (any device, so that
-// the offsets behind it are the same everywhere), the own-keys part, the
-// prefix partials.
-struct SharedWs {
-  size_t own_out, own_lse, meta, part_lse, part_out, total;
-};
-SharedPlan shared_plan(const pa_dims* d, int n_query, int prefix_blocks, int kv_dtype, int sms) {
-  return make_shared_plan((long long)d->num_seqs * n_query * (d->num_q_heads / d->num_kv_heads),
-                          d->num_kv_heads, (long long)prefix_blocks * d->block_size, kv_dtype, sms);
-}
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Workspace of a shared-prefix call: the decode layout (any device, so that
+// the offsets behind it are the same everywhere), the groups' CTAs, the
+// partials.
+struct SharedWs {
+  size_t meta, part_lse, part_out, total;
+};
+SharedPlan shared_plan(const pa_dims* d, int n_query, int kv_dtype, int sms) {
+  return make_shared_plan(d->num_seqs, n_query * (d->num_q_heads / d->num_kv_heads), d->num_kv_heads,
+                          kv_dtype, sms);
+}
 SharedWs shared_ws(const pa_dims* d, int n_query, const SharedPlan& pl) {
-  const size_t rows = (size_t)d->num_seqs * n_query * d->num_q_heads;
   SharedWs w;
-  w.own_out = align256(ws_size_any_device(d, n_query));
-  w.own_lse = w.own_out + rows * kHeadDim * sizeof(float);
-  w.meta = w.own_lse + align256(rows * sizeof(float));
-  w.part_lse = w.meta + 256;
+  w.meta = align256(ws_size_any_device(d, n_query));
+  w.part_lse = w.meta + align256((size_t)(1 + pl.groups) * 2 * sizeof(int));
   w.part_out = w.part_lse + align256((size_t)pl.part_rows * sizeof(float));
   w.total = w.part_out + (size_t)pl.part_rows * kHeadDim * sizeof(float);
   return w;
@@ -197,8 +195,7 @@ size_t paged_attn_shared_workspace_size(const pa_dims* dims, int32_t n_query,
   if (check_shared(dims, n_query, prefix_blocks) != PA_OK) return 0;
   size_t need = 0;
   for (int kv : {PA_KV_FP16, PA_KV_Q8_0})
-    need = std::max(need, shared_ws(dims, n_query, shared_plan(dims, n_query, prefix_blocks, kv,
-                                                               kMaxPrefixCtas)).total);
+    need = std::max(need, shared_ws(dims, n_query, shared_plan(dims, n_query, kv, kMaxPrefixCtas)).total);
   return need;
 }
 
@@ -218,7 +215,7 @@ int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_c
   if (rc != PA_OK) return rc;
   const int sms = device_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
-  const SharedPlan spl = shared_plan(dims, n_query, prefix_blocks, kv_dtype, sms);
+  const SharedPlan spl = shared_plan(dims, n_query, kv_dtype, sms);
   const SharedWs w = shared_ws(dims, n_query, spl);
   if (dims->workspace_bytes < w.total) return PA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(dims->workspace);
@@ -228,6 +225,7 @@ int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_c
   p.v = v_cache;
   p.prefix_table = prefix_table;
   p.prefix_len = prefix_len;
+  p.block_table = block_table;
   p.context_lens = context_lens;
   p.num_seqs = dims->num_seqs;
   p.num_q_heads = dims->num_q_heads;
@@ -244,24 +242,19 @@ int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_c
   p.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;  // as in enqueue_decode
   p.rows_head = spl.rows_head;
   p.row_tile = spl.row_tile;
+  p.rows_seq = spl.rows_seq;
+  p.parts = spl.parts;
+  p.rows_part = spl.rows_part;
+  p.own_row0 = spl.own_row0;
   p.ctas = spl.ctas;
   p.wait_limit_ns = wait_limit_ns();
-  p.own_out = reinterpret_cast<float*>(ws + w.own_out);
-  p.own_lse = reinterpret_cast<float*>(ws + w.own_lse);
   p.part_out = reinterpret_cast<float*>(ws + w.part_out);
   p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   p.meta = reinterpret_cast<int*>(ws + w.meta);
   p.flags = reinterpret_cast<unsigned*>(ws);
   p.out = static_cast<__half*>(out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_prefix_tc(p, st) != cudaSuccess) return PA_ERR_CUDA;
-  PartialArgs own;
-  own.prefix_len = prefix_len;
-  own.out = p.own_out;
-  own.out_lse = p.own_lse;
-  rc = enqueue_decode(dims, plan, q, k_cache, v_cache, block_table, context_lens, n_query, causal,
-                      window, scale, kv_dtype, nullptr, dims->workspace, nullptr, st, own);
-  if (rc != PA_OK) return rc;
+  if (launch_shared_tc(p, st) != cudaSuccess) return PA_ERR_CUDA;
   return launch_shared_join(p, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -101,11 +101,6 @@ struct DecodeParams {
   const int32_t* key_count;
   float* out_f32;
   float* out_lse;
-  // Own-keys mode (shared-prefix decode): the keys of every sequence are
-  // limited to [*prefix_len, L_s), found through its ordinary block_table
-  // row; fp32 outputs as in partial mode, with a NaN log-sum-exp for a row
-  // whose keys reach an out-of-range block.
-  const int32_t* prefix_len;  // null: no shared prefix
   int32_t* trace;             // null, or [B][nq][Hq][5] key-resolution record
   int coop;                   // every CTA of the grid is resident at once
 };

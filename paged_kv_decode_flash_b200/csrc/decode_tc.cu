@@ -327,11 +327,6 @@ __device__ __forceinline__ SeqVis seq_vis(const DecodeParams& p, int s, int L) {
   } else {
     ok = context_len_ok(L, p.n_query, p.max_blocks_per_seq, p.block_size);
   }
-  int own = 0;  // own-keys mode: the first key behind the shared prefix
-  if (p.prefix_len != nullptr) {
-    own = ld_nc_s32(p.prefix_len);
-    ok = ok && own >= 0 && own <= L && own % p.block_size == 0;
-  }
   if (!ok) {
     v.bad = true;
     return v;
@@ -341,7 +336,6 @@ __device__ __forceinline__ SeqVis seq_vis(const DecodeParams& p, int s, int L) {
     v.lo = max(v.lo, kb);
     v.hi = min(v.hi, kb + kc - 1);
   }
-  v.lo = max(v.lo, own);
   v.kb = kb;
   v.base = (v.lo / kChunk) * kChunk;
   if (v.hi >= v.lo) v.nch = (v.hi + 1 - v.base + kChunk - 1) / kChunk;
@@ -490,9 +484,7 @@ __device__ __forceinline__ void merge_pairs(const DecodeParams& p, long long slo
         // holds the row's first column
         const int r = r_lo + j;
         if (p.out_lse != nullptr && r < rows && r * kRowF4 >= pa && r * kRowF4 < pb)
-          p.out_lse[out_row(p, s, kvh, h, r)] =
-              sum > 0.f ? M + logf(sum)
-                        : (bad && p.prefix_len != nullptr) ? __uint_as_float(kInvalidLse) : -INFINITY;
+          p.out_lse[out_row(p, s, kvh, h, r)] = sum > 0.f ? M + logf(sum) : -INFINITY;
       }
     }
     cp_async_wait_all();
@@ -658,7 +650,7 @@ __global__ void __launch_bounds__(Cfg<RW, NG, KV>::kThreads, 1)
       m0_s = sigma / H;
       m0_h = sigma % H;
       m0_L = ld_nc_s32(p.context_lens + m0_s);
-      if (p.window == 0 && p.key_begin == nullptr && p.prefix_len == nullptr) {
+      if (p.window == 0 && p.key_begin == nullptr) {
         const long long nch_s = (long long)p.max_blocks_per_seq * p.block_size / kChunk;
         const long long Ws = (long long)Hkv * nch_s;
         const int Ces = (int)(Ws < (long long)p.ctas_per_set ? Ws : (long long)p.ctas_per_set);

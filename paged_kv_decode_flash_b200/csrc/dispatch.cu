@@ -227,13 +227,12 @@ int enqueue_decode(const pa_dims* d, const Plan& plan, const void* q, const void
   p.trace = trace;
   p.key_begin = partial.key_begin;
   p.key_count = partial.key_count;
-  p.prefix_len = partial.prefix_len;
   p.out_f32 = partial.out;
   p.out_lse = partial.out_lse;
   if (plan.mode == 0) {
-    // Every key of the context (no context-parallel key range, no shared
-    // prefix): the per-head split kernel where the plan chose it.
-    if (plan.split_ctas > 0 && partial.out == nullptr)
+    // Every key of the context (no context-parallel key range): the per-head
+    // split kernel where the plan chose it.
+    if (plan.split_ctas > 0 && partial.key_begin == nullptr)
       return launch_split_decode(p, plan.split_ctas, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     return launch_decode_tc(p, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
@@ -252,8 +251,6 @@ int enqueue_decode(const pa_dims* d, const Plan& plan, const void* q, const void
     if (p.key_begin != nullptr) {
       pl.key_begin = p.key_begin + s0;
       pl.key_count = p.key_count + s0;
-    }
-    if (p.out_f32 != nullptr) {
       pl.out_f32 = p.out_f32 + (long long)s0 * rows_per_seq * kHeadDim;
       pl.out_lse = p.out_lse + (long long)s0 * rows_per_seq;
     }

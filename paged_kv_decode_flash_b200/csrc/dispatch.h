@@ -49,12 +49,10 @@ unsigned long long wait_limit_ns();
 unsigned long long set_wait_limit_ns(unsigned long long ns);
 
 // Partial mode (context-parallel decode): every pointer null, or the key
-// range of each sequence and the fp32 outputs (see DecodeParams).  Own-keys
-// mode (shared-prefix decode): prefix_len and the fp32 outputs.
+// range of each sequence and the fp32 outputs (see DecodeParams).
 struct PartialArgs {
   const int32_t* key_begin = nullptr;
   const int32_t* key_count = nullptr;
-  const int32_t* prefix_len = nullptr;
   float* out = nullptr;
   float* out_lse = nullptr;
 };

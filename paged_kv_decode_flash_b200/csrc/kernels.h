@@ -46,15 +46,18 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, cudaStream_t stream);
 
-// Shared-prefix decode: the prefix part of every query row (prefix_tc.cu) and
-// its join (shared_prefix.cu) with the own-keys part (launch_decode_tc in
-// own-keys mode).
+// Shared-prefix decode: partials of the prefix's and of the sequences' own keys
+// (shared_tc.cu) and their join (shared_prefix.cu).
 constexpr int kMaxPrefixCtas = 160;  // bound of the grid, whatever the device
 struct SharedPlan {
   int rows_head;        // query rows of a KV head: sequences x tokens x group
-  int row_tile;         // of one CTA: 128 or 256
+  int row_tile;         // prefix: rows of a group, 128 or 256
+  int rows_seq;         // rows of a sequence on a KV head: tokens x group
+  int parts, rows_part; // own keys: these in `parts` groups of at most 128
   int ctas;
+  long long own_row0;   // first row of the own-keys partials
   long long part_rows;  // rows of part_out
+  long long groups;     // prefix and own groups
 };
 struct SharedParams {
   const __half* q;              // [B][nq][Hq][D]
@@ -62,17 +65,17 @@ struct SharedParams {
   const void* v;
   const int32_t* prefix_table;  // [prefix_blocks]
   const int32_t* prefix_len;    // [1]
+  const int32_t* block_table;   // [B][mbps]
   const int32_t* context_lens;  // [B]
   int num_seqs, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq;
   int num_blocks, n_query, causal, window, kv_dtype, group, prefix_blocks;
   float scale_log2;             // scale * log2(e)
-  int rows_head, row_tile, ctas;// SharedPlan
+  int rows_head, row_tile, rows_seq, parts, rows_part, ctas;  // SharedPlan
+  long long own_row0;
   unsigned long long wait_limit_ns;
-  float* part_out;              // prefix partials [slots][row_tile][D]
-  float* part_lse;              // [slots][row_tile], natural log
-  int* meta;                    // [2] key tiles of the prefix, CTAs that worked
-  float* own_out;               // own-keys part [rows][D]
-  float* own_lse;               // [rows], natural log
+  float* part_out;              // partials [slots][row_tile][D], [own slots][rows_part][D]
+  float* part_lse;              // natural log
+  int* meta;                    // key tiles of the prefix, -; first and last CTA of every group
   unsigned* flags;              // workspace status word
   __half* out;                  // [B][nq][Hq][D]
 };
@@ -83,9 +86,8 @@ __host__ __device__ __forceinline__ bool shared_prefix_ok(const SharedParams& p,
 __host__ __device__ __forceinline__ bool shared_seq_ok(const SharedParams& p, int L, int P) {
   return context_len_ok(L, p.n_query, p.max_blocks_per_seq, p.block_size) && P <= L;
 }
-SharedPlan make_shared_plan(long long rows_head, int num_kv_heads, long long prefix_keys, int kv_dtype,
-                            int sms);
-cudaError_t launch_prefix_tc(const SharedParams& p, cudaStream_t stream);
+SharedPlan make_shared_plan(int num_seqs, int rows_seq, int num_kv_heads, int kv_dtype, int sms);
+cudaError_t launch_shared_tc(const SharedParams& p, cudaStream_t stream);
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
 
 // Page operations (pages.cu).

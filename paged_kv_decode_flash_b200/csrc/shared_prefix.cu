@@ -6,10 +6,9 @@
 // z_j = scale q.k_j, m_X = max_X z and l_X = sum_X e^(z_j - m_X):
 //   out = (e^(m_A - m) l_A O_A + e^(m_B - m) l_B O_B) /
 //         (e^(m_A - m) l_A + e^(m_B - m) l_B),   m = max(m_A, m_B),
-// where O_X = sum_X e^(z_j - m_X) v_j / l_X.  The prefix part comes in pieces,
-// one per CTA that had some of its keys (prefix_tc.cu), the own-keys part
-// (O_B, lse_B) from the segment kernel (decode_tc.cu, own-keys mode); this
-// file has the work plan and the join.
+// where O_X = sum_X e^(z_j - m_X) v_j / l_X.  Both come in pieces, one per CTA
+// that had some of the keys (shared_tc.cu); this file has the work plan and
+// the join.
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -19,56 +18,65 @@ namespace {
 
 using namespace sm100;
 
-// The join: one warp per output row over the row's prefix partials and its
-// own-keys partial, weights e^(lse - max).  A NaN log-sum-exp (an
-// out-of-range block, a timeout) and a bad length give a row of zeros.
+// The join: one warp per output row over the row's partials, weights
+// e^(lse - max).  A NaN log-sum-exp (an out-of-range block, a timeout) and a
+// bad length give a row of zeros.
 __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
   const long long rows = (long long)p.num_seqs * p.n_query * p.num_q_heads;
   const long long row = (long long)blockIdx.x * 4 + threadIdx.x / 32;
+  const int hq = (int)(row % p.num_q_heads), kvh = hq / p.group;
+  const int tok = (int)(row / p.num_q_heads), s = tok / p.n_query;
+  const int rh = tok * p.group + hq % p.group;  // row of the KV head
+  const int NT = (p.rows_head + p.row_tile - 1) / p.row_tile;
+  const int rs = rh - s * p.rows_seq, part = rs / p.rows_part;
+  const int gp = kvh * NT + rh / p.row_tile, go = s * p.num_kv_heads * p.parts + kvh * p.parts + part;
+  griddep_wait();
+  griddep_launch_dependents();
   if (row >= rows) return;
-  const int s = (int)(row / ((long long)p.num_q_heads * p.n_query));
-  const int P = __ldg(p.prefix_len), L = __ldg(p.context_lens + s);
+  const int P = __ldg(p.prefix_len), L = __ldg(p.context_lens + s), nt = __ldcg(p.meta);
+  const int2 cp = __ldcg(reinterpret_cast<const int2*>(p.meta) + 1 + gp);
+  const int2 co = __ldcg(reinterpret_cast<const int2*>(p.meta) + 1 + p.num_kv_heads * NT + go);
   bool ok = shared_prefix_ok(p, P);
   if (!ok && row == 0 && lane == 0) atomicOr(p.flags, kFlagBadLen);
-  ok = ok && shared_seq_ok(p, L, P);
-  // The row's partials: slots c + g of the CTAs c that cut its group's tiles.
-  const int nt = __ldcg(p.meta), Ce = __ldcg(p.meta + 1);
-  const int hq = (int)(row % p.num_q_heads), kvh = hq / p.group;
-  const long long rh = row / p.num_q_heads * p.group + hq % p.group;
-  const int NT = (p.rows_head + p.row_tile - 1) / p.row_tile;
-  const int g = kvh * NT + (int)(rh / p.row_tile);
-  int c0 = 0, n = 0;
-  if (nt > 0) {
-    const long long W = (long long)p.num_kv_heads * NT * nt, x0 = (long long)g * nt;
-    c0 = (int)(((x0 + 1) * Ce - 1) / W);
-    n = (int)(((x0 + nt) * Ce - 1) / W) - c0 + 1;
+  if (ok && !shared_seq_ok(p, L, P)) {
+    ok = false;
+    if (lane == 0) atomicOr(p.flags, kFlagBadLen);
   }
-  const long long at = (long long)(c0 + g) * p.row_tile + rh % p.row_tile;  // + k * row_tile
-  float M = -INFINITY;
+  // The row's partials: np of the prefix, then no of its own keys.
+  int np = 0, no = 0;
+  if (ok) {
+    if (nt > 0) np = cp.y - cp.x + 1;
+    int lo, hi;
+    union_range(L, p.n_query, p.causal, p.window, lo, hi);
+    if (hi >= max(lo, P)) no = co.y - co.x + 1;
+  }
+  const long long at_p = (long long)(cp.x + gp) * p.row_tile + rh % p.row_tile;
+  const long long at_o = p.own_row0 + (long long)(co.x + go) * p.rows_part + rs % p.rows_part;
+  auto slot = [&](int k) {
+    return k < np ? at_p + (long long)k * p.row_tile : at_o + (long long)(k - np) * p.rows_part;
+  };
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
   bool bad = false;
-  for (int k = lane; k <= n; k += 32) {
-    const float e = k < n ? __ldcg(p.part_lse + at + (long long)k * p.row_tile) : __ldcg(p.own_lse + row);
-    bad |= isnan(e);
-    M = fmaxf(M, e);
-  }
+  for (int k0 = 0; k0 < np + no; k0 += 32) {  // 32 partials at a time, lane k their lse
+    const int n = min(32, np + no - k0);
+    const float e = lane < n ? __ldcg(p.part_lse + slot(k0 + lane)) : -INFINITY;
+    bad |= __any_sync(0xffffffffu, isnan(e));
+    float mx = fmaxf(e, M);
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-  bad = __any_sync(0xffffffffu, bad);
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  if (ok && !bad && M != -INFINITY) {
-#pragma unroll 4
-    for (int k = 0; k <= n; ++k) {
-      const bool own = k == n;
-      const long long slot = at + (long long)k * p.row_tile;
-      const float e = own ? __ldcg(p.own_lse + row) : __ldcg(p.part_lse + slot);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(own ? p.own_out + row * kHeadDim
-                                                                  : p.part_out + slot * kHeadDim) +
-                              lane);
-      if (e == -INFINITY) continue;
-      const float w = expf(e - M);
+    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+    if (mx == -INFINITY) continue;
+    const float f = expf(M - mx), we = expf(e - mx);
+    M = mx;
+    l *= f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] *= f;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float w = __shfl_sync(0xffffffffu, we, k);
+      const float4 v =
+          __ldcg(reinterpret_cast<const float4*>(p.part_out + slot(k0 + k) * kHeadDim) + lane);
+      if (w == 0.f) continue;  // (a partial without keys)
       l += w;
       o[0] = fmaf(w, v.x, o[0]);
       o[1] = fmaf(w, v.y, o[1]);
@@ -76,9 +84,10 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
       o[3] = fmaf(w, v.w, o[3]);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const __half2 a = __floats2half2_rn(o[0] * inv, o[1] * inv);
-  const __half2 b = __floats2half2_rn(o[2] * inv, o[3] * inv);
+  const float inv = l > 0.f && !bad ? 1.f / l : 0.f;
+  auto end = [&](float x) { return inv > 0.f ? x * inv : 0.f; };
+  const __half2 a = __floats2half2_rn(end(o[0]), end(o[1]));
+  const __half2 b = __floats2half2_rn(end(o[2]), end(o[3]));
   uint2 u;
   u.x = *reinterpret_cast<const uint32_t*>(&a);
   u.y = *reinterpret_cast<const uint32_t*>(&b);
@@ -101,16 +110,21 @@ cudaError_t launch_pdl(void (*kern)(const SharedParams), dim3 grid, const Shared
 
 }  // namespace
 
-SharedPlan make_shared_plan(long long rows_head, int num_kv_heads, long long prefix_keys, int kv_dtype,
-                            int sms) {
+SharedPlan make_shared_plan(int num_seqs, int rows_seq, int num_kv_heads, int kv_dtype, int sms) {
   SharedPlan pl;
-  pl.rows_head = (int)rows_head;
-  pl.row_tile = kv_dtype == kKvFp16 && rows_head > 128 ? 256 : 128;
-  const long long groups = num_kv_heads * ((rows_head + pl.row_tile - 1) / pl.row_tile);
-  const long long tiles = groups * (prefix_keys / kTileKeys + 2);
-  const long long most = sms < kMaxPrefixCtas ? sms : kMaxPrefixCtas;
-  pl.ctas = (int)(tiles < most ? tiles : most);
-  pl.part_rows = (pl.ctas + groups) * pl.row_tile;
+  pl.rows_head = num_seqs * rows_seq;
+  // 256 rows on a K and a V tile halve the traffic to shared memory; the int8
+  // caches' converted tiles leave room for 128.
+  pl.row_tile = kv_dtype == kKvFp16 && pl.rows_head > 128 ? 256 : 128;
+  pl.rows_seq = rows_seq;
+  pl.parts = (rows_seq + 127) / 128;
+  pl.rows_part = (rows_seq + pl.parts - 1) / pl.parts;
+  pl.ctas = sms < kMaxPrefixCtas ? sms : kMaxPrefixCtas;
+  const long long gp = (long long)num_kv_heads * ((pl.rows_head + pl.row_tile - 1) / pl.row_tile);
+  const long long go = (long long)num_seqs * num_kv_heads * pl.parts;
+  pl.own_row0 = (pl.ctas + gp) * pl.row_tile;
+  pl.part_rows = pl.own_row0 + (pl.ctas + go) * pl.rows_part;
+  pl.groups = gp + go;
   return pl;
 }
 
