@@ -15,17 +15,17 @@
 // (WorkCut below) and cut into equal ranges over the CTAs (one per SM); a
 // CTA's run of tiles of one group is a segment and makes one partial per row.
 //
-// A CTA has two streams, each a softmax warpgroup (thread = query row), an
-// S / P buffer and an O accumulator of 128 x 128 in TMEM, so that the tensor
-// cores work for one stream while the other's softmax runs:
+// A CTA has two streams, each a softmax warpgroup (thread = query row) and an
+// O accumulator of 128 x 128 in TMEM:
 //   dual segment (more than 128 rows): stream w has rows 128 w .. and every
-//           key tile (a K and a V tile in shared memory serve 256 rows);
-//   single: both streams have the same rows, stream w every other key tile;
-//           their sums are joined at the segment's end.
-// S = Q K^T (M = 128 rows, N = 128 keys), P overwrites S in TMEM as fp16
-// high parts and residuals (the weights to 2^-22, as in the other decode
-// kernels), and O += [P_hi | P_lo] V takes P from TMEM and V as it lies in
-// the cache.
+//           key (a K and a V tile in shared memory serve 256 rows);
+//   single: both streams have the same rows, stream w keys 64 w .. of every
+//           tile; their sums are joined at the segment's end.
+// A stream works in steps of 64 keys with two S / P buffers of 64 columns, so
+// that its next scores are there when a step's softmax ends: S = Q K^T
+// (M = 128 rows, N = 64 keys), P overwrites S in TMEM as fp16 high parts and
+// residuals (the weights to 2^-22, as in the other decode kernels), and
+// O += [P_hi | P_lo] V takes P from TMEM and V as it lies in the cache.
 //
 // The int8 caches are converted on the way in, to operands that lose nothing
 // that matters:
@@ -38,11 +38,12 @@
 // They run single segments only: 128 rows leave shared memory for the
 // converted tiles.
 //
-// Roles: warps 0-3 and 4-7 the softmax warpgroups, which also stage Q and
-// write the partials.  fp16: warp 8 K producer, warp 9 V producer (TMA boxes
-// of 16 keys through the block table), warp 10 MMA issuer.  int8: warps 8-11
-// converters (raw bytes through registers, one tile ahead), warp 12 MMA
-// issuer.  The next warp cuts the CTA's range into segments.
+// Roles: warps 0-7 the softmax, which also stages Q and writes the partials.
+// Then, fp16: a producer (TMA boxes of 16 keys through the block table);
+// int8: four converters (raw bytes through registers, one tile ahead).  Then
+// an MMA issuer for each stream (one for both was the bottleneck: with the
+// waits, a step's sixteen products take a warp 1750 cycles to issue and the
+// tensor cores 780), and a warp that cuts the CTA's range into segments.
 //
 // Every wait is bounded (SharedParams::wait_limit_ns): on a timeout the
 // kernel raises kFlagTimeout, drains its copies and MMAs with a fixed bound,
@@ -68,15 +69,16 @@ constexpr uint32_t kAtomBytes = 1024;
 constexpr uint32_t kGroupBytes = 2 * kAtomBytes;
 constexpr uint32_t kTileBytes = kTileKeys / 8 * kGroupBytes;  // 32 KB
 constexpr uint32_t kChunkBytes = kChunk * 256;
-// Weights are scaled by 2^kShift and stay below 2^(kShift + kLazy) < 65504.
-// A large kLazy makes rescaling rare; what it costs are weights 2^-25 below
-// the reference's, which fp16's range cuts off.
+// Weights are scaled by 2^kShift.  A row keeps its reference while the sum of
+// a step's weights stays below kSumLimit, so that each is inside fp16's range;
+// what the large limit costs are weights 2^-27 below the reference's, which
+// fp16's range cuts off.
 constexpr float kShift = 2.f;
-constexpr float kLazy = 13.f;
+constexpr float kSumLimit = 32768.f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kInvalidLse = 0x7fc00000u;  // NaN: a partial that must not be used
-constexpr int kInfoSlots = 16;
-constexpr int kOwnStart = 1;    // what the start of an own-keys segment costs, in units
+constexpr int kStep = 64;       // keys of a step of a stream
+constexpr int kOwnStart = 4;    // what the start of an own-keys segment costs, in units
 constexpr int kScaleSlots = 8;  // tiles whose row scales are kept: more than are in flight
 
 constexpr int kSegSlots = 4;
@@ -86,24 +88,25 @@ enum : int {
   BAR_KEMPTY = 3,  // [3]
   BAR_VFULL = 6,   // [3]
   BAR_VEMPTY = 9,  // [3]
-  BAR_SFULL = 12,  // [2] S of a stream's unit in TMEM
-  BAR_PFULL = 14,  // [2] P of a stream's unit in TMEM
-  BAR_QFULL = 16,  // a segment's Q staged, the previous one's O read
-  BAR_SEG = 17,    // every MMA of a segment finished
-  BAR_DONE = 18,
-  BAR_GFULL = 19,  // [kSegSlots] a segment's description published
-  BAR_GEMPTY = 23, // [kSegSlots] ... read by every role
-  BAR_COUNT = 27
+  BAR_SFULL = 12,  // [stream][buffer] S of a step in TMEM
+  BAR_PFULL = 16,  // [stream][buffer] P of a step in TMEM
+  BAR_OFULL = 20,  // [stream] PV of all of a segment's steps but the last accumulated
+  BAR_QFULL = 22,  // a segment's Q staged, the previous one's O read
+  BAR_SEG = 23,    // every MMA of a segment finished
+  BAR_DONE = 24,
+  BAR_GFULL = 25,  // [kSegSlots] a segment's description published
+  BAR_GEMPTY = 29, // [kSegSlots] ... read by every role
+  BAR_COUNT = 33
 };
 
 template <int KV>
 struct Cfg {
   static constexpr bool kQuant = KV != kKvFp16;
   static constexpr bool kQ8 = KV == kKvQ8_0, kRow = KV == kKvInt8Row;
-  static constexpr int kProdWarp = 8;                      // fp16: K, V producer; int8: converters
-  static constexpr int kMmaWarp = kQuant ? 12 : 10;
-  static constexpr int kReaders = kMmaWarp + 1;            // warps that follow the segments
-  static constexpr int kThreads = kQuant ? 448 : 384;
+  static constexpr int kProdWarp = 8;                      // fp16: producer; int8: converters
+  static constexpr int kMmaWarp = kProdWarp + (kQuant ? 4 : 1);  // [2], then the segments' warp
+  static constexpr int kReaders = kMmaWarp + 2;            // warps that follow the segments
+  static constexpr int kThreads = kQuant ? 480 : 384;
   static constexpr uint32_t kSlot = (kQ8 ? 2 : 1) * kTileBytes;  // q8_0: the high tile, the residual
   static constexpr int KS = kQ8 ? 1 : kRow ? 2 : 3;
   static constexpr int VS = kRow ? 3 : 2;
@@ -111,8 +114,7 @@ struct Cfg {
   static constexpr uint32_t kK = kQ + (kQuant ? 1 : 2) * kTileBytes;
   static constexpr uint32_t kV = kK + KS * kSlot;
   static constexpr uint32_t kBars = kV + VS * kSlot;
-  static constexpr uint32_t kInfo = kBars + BAR_COUNT * 8 + 8;      // uint32 [kInfoSlots]
-  static constexpr uint32_t kMisc = kInfo + kInfoSlots * 4;         // int [16], see below
+  static constexpr uint32_t kMisc = kBars + BAR_COUNT * 8 + 8;         // int [16], see below
   static constexpr uint32_t kSegs = kMisc + 64;             // Segment [kSegSlots]
   static constexpr uint32_t kScales = kSegs + kSegSlots * 64;  // int8 rows: float K [8][128], V [8][128], max [8][4]
   static constexpr uint32_t kTotal = kScales + (kRow ? kScaleSlots * (2 * 128 + 4) * 4 : 0);
@@ -127,6 +129,14 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
 // Four signed bytes -> four exact fp16 values: byte b becomes the low mantissa
 // byte of the fp16 1024 + (b + 128), minus 1152.
 __device__ __forceinline__ void q8_to_half4(uint32_t q, __half2& lo, __half2& hi) {
@@ -137,6 +147,20 @@ __device__ __forceinline__ void q8_to_half4(uint32_t q, __half2& lo, __half2& hi
   hi = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
 }
 
+// x - h for two fp16 values (exact).
+__device__ __forceinline__ float2 residual(float2 x, uint32_t h) {
+  float2 d;
+  asm("{\n\t.reg .b16 a, b, m;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 m, 0xBC00;\n\t"  // -1
+      "fma.rn.f32.f16 %0, a, m, %3;\n\tfma.rn.f32.f16 %1, b, m, %4;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(h), "f"(x.x), "f"(x.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -194,9 +218,9 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + C::kQ, sK = sbase + C::kK, sV = sbase + C::kV;
-  uint32_t* info = reinterpret_cast<uint32_t*>(smem + C::kInfo);
-  // [0] TMEM base, [1] abort, [2] shortest sequence, [3] start sequence,
-  // [4, 5] its start, [6, 7] own units of the batch, [8] segments given up
+    // [0] TMEM base, [1] abort, [2] shortest sequence, [3] start sequence,
+  // [4, 5] its start, [6, 7] own units of the batch, [8] segments given up,
+  // [9] a block was out of range
   int* misc = reinterpret_cast<int*>(smem + C::kMisc);
   volatile int* abort = misc + 1;
   const unsigned long long wl = p.wait_limit_ns;
@@ -208,20 +232,22 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < BAR_COUNT; ++i)
       mbar_init(bar(i), i == BAR_QFULL                                                   ? 8
-                        : (i == BAR_PFULL || i == BAR_PFULL + 1)                         ? 4
-                        : (kQuant && (i < BAR_KEMPTY || (i >= BAR_VFULL && i < BAR_VEMPTY))) ? 4
+                        : (i >= BAR_PFULL && i < BAR_OFULL)                              ? 4
+                        : (i < BAR_SFULL && (i % 6 >= 3 || kQuant)) ? (i % 6 >= 3 ? 2 : 4)  // empty, full
+                        : i == BAR_SEG || i == BAR_DONE                                  ? 2
                         : i >= BAR_GEMPTY                                                ? C::kReaders
                                                                                          : 1);
     misc[1] = 0;
     misc[2] = INT32_MAX;
     misc[8] = 0;
+    misc[9] = 0;
     misc[3] = p.num_seqs;
     *reinterpret_cast<unsigned long long*>(misc + 6) = 0;
     fence_mbar_init();
   }
   if (warp == C::kMmaWarp) tmem_alloc(smem_u32(misc), 512);
   if constexpr (!kQuant) {
-    if (threadIdx.x == 256) {
+    if (threadIdx.x == 32 * C::kProdWarp) {
       prefetch_tmap(&tmap_k);
       prefetch_tmap(&tmap_v);
     }
@@ -337,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     for (int i = 0;; ++i) {
       if (!__all_sync(0xffffffffu, seg_wait(BAR_GFULL + i % kSegSlots, i / kSegSlots))) break;
       const Segment& g = segs[i % kSegSlots];
-      if (g.n == 0) break;
+      if (__reduce_max_sync(0xffffffffu, g.n) == 0) break;
       f(g);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_GEMPTY + i % kSegSlots));
@@ -454,9 +480,9 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           const int sk = T % C::KS, sv = T % C::VS, ss = T % kScaleSlots;
           ok = ok && __all_sync(0xffffffffu, wait(BAR_KEMPTY + sk, (T / C::KS) ^ 1));
           if (!ok) break;
-          if (lane == 0) {
-            reinterpret_cast<uint8_t*>(info + T % kInfoSlots)[cw] = (uint8_t)bad;
-            if (bad) atomicOr(p.flags, kFlagBadBlock);
+          if (bad && lane == 0) {
+            misc[9] = 1;
+            atomicOr(p.flags, kFlagBadBlock);
           }
           if constexpr (kRow) scales[ss * 128 + 32 * cw + lane] = k.d1 * cs;
           convert(k, sK + sk * C::kSlot, kw, 0);
@@ -484,130 +510,169 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
         }
       });
     }
-  } else if (warp == C::kProdWarp || warp == C::kProdWarp + 1) {
-    // ===================== K and V producers ================================
-    const bool isk = warp == C::kProdWarp;
-    const int NS = isk ? C::KS : C::VS;
-    const uint32_t ring = isk ? sK : sV;
-    const int full = isk ? BAR_KFULL : BAR_VFULL, empty = isk ? BAR_KEMPTY : BAR_VEMPTY;
-    const CUtensorMap* tmap = isk ? &tmap_k : &tmap_v;
-    int T = 0;  // tiles issued
+  } else if (warp == C::kProdWarp) {
+    // ===================== K and V producer =================================
+    int TK = 0, TV = 0;  // tiles issued
     bool ok = true;
-    constexpr int kNone = INT32_MIN;
     segments([&](const Segment& g) {
-      const int kvh = g.kvh, base = g.base, t0 = g.t0, n = g.n, vhi = g.hi;
-      const int32_t* table = g.table;
-      auto lookup = [&](int t) -> int {
+      const int base = g.base, t0 = g.t0, n = g.n, vhi = g.hi;
+      // Lane's chunk of tile t: its TMA row coordinate (-1: none).
+      auto row8_of = [&](int t, bool& bad) -> int {
         const int key0 = base + t * kTileKeys + lane * kChunk;
-        if (lane >= kChunksPerTile || t >= t0 + n || key0 > vhi) return kNone;
-        return __ldg(table + key0 / p.block_size);
+        if (lane >= kChunksPerTile || key0 > vhi) return -1;
+        int phys = __ldg(g.table + key0 / p.block_size);
+        bad = phys < 0 || phys >= p.num_blocks;
+        if (bad) phys = 0;  // a stand-in: the rows that see it are marked
+        return (int)((((long long)phys * p.num_kv_heads + g.kvh) * p.block_size + key0 % p.block_size) / 8);
       };
-      int raw = lookup(t0);
-      for (int t = t0; t < t0 + n && ok; ++t, ++T) {
-        const int next = lookup(t + 1);
-        bool bad = false;
-        int row8 = -1;
-        const int key0 = base + t * kTileKeys + lane * kChunk;
-        if (raw != kNone || (lane < kChunksPerTile && key0 <= vhi)) {
-          int phys = raw;
-          bad = phys < 0 || phys >= p.num_blocks;
-          if (bad) phys = 0;  // a stand-in: the rows that see it are marked
-          row8 = (int)((((long long)phys * p.num_kv_heads + kvh) * p.block_size + key0 % p.block_size) / 8);
-        }
+      auto issue = [&](bool isk, int T, int row8) {
+        const int st = isk ? T % C::KS : T % C::VS, full = (isk ? BAR_KFULL : BAR_VFULL) + st;
         const uint32_t mask = __ballot_sync(0xffffffffu, row8 >= 0);
-        const uint32_t badmask = __ballot_sync(0xffffffffu, bad);
-        const int st = T % NS;
-        int w = 1;
-        if (lane == 0) w = wait(empty + st, (T / NS) ^ 1);
-        ok = __shfl_sync(0xffffffffu, w, 0) != 0;
-        if (!ok) break;
-        if (lane == 0) {
-          if (isk) {
-            info[T % kInfoSlots] = badmask;
-            if (badmask) atomicOr(p.flags, kFlagBadBlock);
-          }
-          mbar_arrive_expect_tx(bar(full + st), __popc(mask) * kChunkBytes);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(full), __popc(mask) * kChunkBytes);
         __syncwarp();
         if (row8 >= 0)
-          tma_load_4d(ring + st * C::kSlot + lane * kChunkBytes, tmap, 0, 0, 0, row8, bar(full + st));
+          tma_load_4d((isk ? sK : sV) + st * C::kSlot + lane * kChunkBytes, isk ? &tmap_k : &tmap_v, 0, 0,
+                      0, row8, bar(full));
         __syncwarp();
-        raw = next;
+      };
+      int jk = 0, jv = 0;  // tiles of the segment issued
+      bool badk = false, badv = false;
+      int rk = row8_of(t0, badk), rv = rk;  // of tiles jk, jv
+      while (ok && jv < n) {
+        // Whichever slot is free; K leads.
+        bool k = false, v = false;
+        unsigned long long since = 0;
+        for (;;) {
+          k = jk < n && mbar_test_wait(bar(BAR_KEMPTY + TK % C::KS), ((TK / C::KS) & 1) ^ 1);
+          v = jv < jk && mbar_test_wait(bar(BAR_VEMPTY + TV % C::VS), ((TV / C::VS) & 1) ^ 1);
+          k = __any_sync(0xffffffffu, k);
+          v = __any_sync(0xffffffffu, v);
+          if (k || v) break;
+          const unsigned long long now = globaltimer();
+          if (since == 0) since = now;
+          if (now - since > wl) *abort = 1;
+          if (__any_sync(0xffffffffu, *abort != 0)) break;
+          __nanosleep(64);
+        }
+        ok = k || v;
+        if (k) {
+          if (badk) {
+            misc[9] = 1;
+            atomicOr(p.flags, kFlagBadBlock);
+          }
+          issue(true, TK++, rk);
+          badk = false;
+          if (++jk < n) rk = row8_of(t0 + jk, badk);
+        }
+        if (v) {
+          issue(false, TV++, rv);
+          if (++jv < n) rv = row8_of(t0 + jv, badv);
+        }
       }
     });
     // No copy outlives the CTA: the last of every slot (landed already unless
     // a wait gave up).
     if (lane == 0) {
       volatile int no_abort = 0;
-      for (int u = max(0, T - NS); u < T; ++u) mbar_wait(bar(full + u % NS), (u / NS) & 1, &no_abort);
+      for (int u = max(0, TK - C::KS); u < TK; ++u)
+        mbar_wait(bar(BAR_KFULL + u % C::KS), (u / C::KS) & 1, &no_abort);
+      for (int u = max(0, TV - C::VS); u < TV; ++u)
+        mbar_wait(bar(BAR_VFULL + u % C::VS), (u / C::VS) & 1, &no_abort);
     }
   }
-  if (warp == C::kMmaWarp) {
-    // ===================== MMA issuer =======================================
-    const uint32_t id_qk = idesc_f16_f32(128, 128, false, false);
+  if (warp == C::kMmaWarp || warp == C::kMmaWarp + 1) {
+    // ===================== MMA issuers ======================================
+    const int w = warp - C::kMmaWarp;  // the stream
+    const uint32_t id_qk = idesc_f16_f32(128, kStep, false, false);
     const uint32_t id_pv = idesc_f16_f32(128, 128, false, true);
     const uint64_t dQ = smem_desc(sQ, 16, kGroupBytes, kSwizzle128B);
     const uint64_t dK = smem_desc(sK, 16, kGroupBytes, kSwizzle128B);
     const uint64_t dV = smem_desc(sV, kAtomBytes, kGroupBytes, kSwizzle128B);
-    int T0 = 0, seg = 0, np0 = 0, np1 = 0;  // np: P of each stream
+    constexpr uint32_t kHalfTile = kTileBytes / 2;   // 64 keys
+    // The whole warp runs this code and one elected lane issues: what the
+    // products take stays in uniform registers (a lane on its own spends 126
+    // cycles a product on moving operands there).
+    const uint32_t lead = elect_one();
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem), ob = tm + 256 + w * 128;
+    auto wait1 = [&](int b, int parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+    int ks = 0, kp = 0, vs = 0, vp = 0;  // ring slots and their phases
+    int c = 0, seg = 0;                  // steps and segments before
     bool ok = true;
     segments([&](const Segment& g) {
-      if (!ok || lane != 0) return;
-      const bool dual = !kQuant && (g.flags & kDual);
-      const int n = g.n, X = dual ? 2 * n : n;
-      ok = wait(BAR_QFULL, seg);
       if (!ok) return;
-      tc_fence_after();
-      auto qk = [&](int x) -> bool {
-        const int w = x & 1, T = T0 + (dual ? x >> 1 : x), st = T % C::KS;
-        if ((!dual || w == 0) && !wait(BAR_KFULL + st, T / C::KS)) return false;
-        tc_fence_after();
-        const uint64_t qo = dual ? (uint64_t)(w * kTileBytes) >> 4 : 0;
-        const uint64_t ko = (uint64_t)(st * C::kSlot) >> 4;
+      const int gn = __reduce_max_sync(0xffffffffu, g.n);
+      const bool dual = !kQuant && (__reduce_max_sync(0xffffffffu, g.flags) & kDual);
+      const int Y = dual ? 2 * gn : gn;  // steps of the stream
+      const uint64_t q = dQ + (dual ? (uint64_t)(w * kTileBytes) >> 4 : 0);
+      ok = wait1(BAR_QFULL, seg);
+      if (!ok) return;
+      // S of step y (its buffer (c + y) & 1), products of K's high parts, then
+      // q8_0's residuals.
+      auto scores = [&](int y) {
+        const int half = dual ? y & 1 : w;
+        if (!dual || half == 0) {
+          ok = wait1(BAR_KFULL + ks, kp);
+          if (!ok) return;
+          tc_fence_after();
+        }
+        const uint32_t sb = tm + w * 128 + ((c + y) & 1) * kStep;
+        const uint64_t kd = dK + ((uint64_t)(ks * C::kSlot + half * kHalfTile) >> 4);
 #pragma unroll
-        for (int part = 0; part < (kQ8 ? 2 : 1); ++part)  // high parts, residuals of K
-#pragma unroll
-          for (int k = 0; k < kHeadDim / 16; ++k) {
-            const uint64_t o = ((k / 4) * kAtomBytes + (k % 4) * 32) >> 4;
-            tc_mma_f16_ss(tmem + w * 128, dQ + qo + o, dK + ko + ((part * kTileBytes) >> 4) + o,
-                          id_qk, part > 0 || k > 0);
+        for (int i = 0; i < (kQ8 ? 16 : 8); ++i) {
+          const uint64_t o = ((i % 8 / 4) * kAtomBytes + (i % 4) * 32) >> 4;
+          tc_mma_f16_ss(lead, sb, q + o, kd + ((i / 8 * kTileBytes) >> 4) + o, id_qk, i > 0);
+        }
+        tc_commit(lead, bar(BAR_SFULL + w * 2 + ((c + y) & 1)));
+        if (!dual || half == 1) {
+          tc_commit(lead, bar(BAR_KEMPTY + ks));
+          if (++ks == C::KS) {
+            ks = 0;
+            kp ^= 1;
           }
-        tc_commit(bar(BAR_SFULL + w));
-        if (!dual || w == 1) tc_commit(bar(BAR_KEMPTY + st));
-        return true;
+        }
       };
-      for (int x = 0; x < 2 && x < X && ok; ++x) ok = qk(x);
-      for (int x = 0; x < X && ok; ++x) {
-        const int w = x & 1, T = T0 + (dual ? x >> 1 : x), st = T % C::VS;
-        ok = wait(BAR_PFULL + w, w ? np1 : np0) &&
-             ((dual && w == 1) || wait(BAR_VFULL + st, T / C::VS));
+      scores(0);
+      if (ok && Y > 1) scores(1);
+      for (int y = 0; y < Y && ok; ++y) {
+        const int half = dual ? y & 1 : w, buf = (c + y) & 1;
+        ok = wait1(BAR_PFULL + w * 2 + buf, (c + y) >> 1) &&
+             ((dual && half == 1) || wait1(BAR_VFULL + vs, vp));
         if (!ok) break;
-        w ? ++np1 : ++np0;
         tc_fence_after();
-        const uint64_t vo = (uint64_t)(st * C::kSlot) >> 4;
-        const uint32_t d = tmem + 256 + w * 128;
+        const uint32_t pb = tm + w * 128 + buf * kStep;
+        const uint64_t vd = dV + ((uint64_t)(vs * C::kSlot + half * kHalfTile) >> 4);
         // P_hi V, P_lo V and, q8_0, P_hi V_lo
 #pragma unroll
-        for (int part = 0; part < (kQ8 ? 3 : 2); ++part)
-#pragma unroll
-          for (int k = 0; k < kTileKeys / 16; ++k)
-            tc_mma_f16_ts(d, tmem + w * 128 + (k / 2) * 32 + (part == 1) * 16 + (k % 2) * 8,
-                          dV + vo + ((k * 2 * kGroupBytes + (part == 2) * kTileBytes) >> 4), id_pv,
-                          x > 1 || part > 0 || k > 0);
-        if (!dual || w == 1) tc_commit(bar(BAR_VEMPTY + st));
-        if (x + 2 < X) ok = qk(x + 2);
+        for (int i = 0; i < (kQ8 ? 12 : 8); ++i) {
+          const int part = i / 4, k = i % 4;
+          tc_mma_f16_ts(lead, ob, pb + (k / 2) * 32 + (part == 1) * 16 + (k % 2) * 8,
+                        vd + ((k * 2 * kGroupBytes + (part == 2) * kTileBytes) >> 4), id_pv,
+                        y > 0 || i > 0);
+        }
+        if (!dual || half == 1) {
+          tc_commit(lead, bar(BAR_VEMPTY + vs));
+          if (++vs == C::VS) {
+            vs = 0;
+            vp ^= 1;
+          }
+        }
+        if (y == Y - 2) tc_commit(lead, bar(BAR_OFULL + w));
+        if (y + 2 < Y) scores(y + 2);
       }
-      if (ok) tc_commit(bar(BAR_SEG));
-      T0 += n;
+      if (ok) {
+        if (Y == 1) tc_commit(lead, bar(BAR_OFULL + w));
+        tc_commit(lead, bar(BAR_SEG));
+      }
+      c += Y;
       ++seg;
     });
-    if (lane == 0) {
+    if (lead) {
       tc_commit(bar(BAR_DONE));
       volatile int no_abort = 0;
       mbar_wait(bar(BAR_DONE), 0, &no_abort);
     }
     __syncwarp();
-  } else if (warp == C::kMmaWarp + 1) {
+  } else if (warp == C::kMmaWarp + 2) {
     // ===================== segments =========================================
     if (lane == 0) {
       int count = 0;
@@ -674,25 +739,26 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       publish(end);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < C::kProdWarp) {
     // ===================== softmax warpgroups ===============================
     const int w = warp / 4, r = threadIdx.x % 128;
+    constexpr int kSoftThreads = 256;
     const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
-    const uint32_t tS = tmem + lane_off + w * 128, tO = tmem + lane_off + 256;
+    const uint32_t tO = tmem + lane_off + 256;
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale negates Q
-    int T0 = 0, seg = 0, ns = 0;  // ns: units of this stream
+    int T0 = 0, c0 = 0, seg = 0;  // tiles, steps and segments before
     bool ok = true;
     segments([&](const Segment& g) {
       const bool dual = !kQuant && (g.flags & kDual);
       const int local = (dual ? w * 128 : 0) + r, row = g.row0 + local;
       const bool mine = local < g.nrows;
       const int tok = row / p.group;  // of all sequences' new tokens
-      // ---- Q: this warpgroup's rows (single: half of every row) -------------
+      // ---- Q: this warpgroup's share of the rows' columns ---------------------
       {
         const __half* src = p.q + ((long long)(mine ? tok : 0) * p.num_q_heads + g.kvh * p.group +
                                    (mine ? row % p.group : 0)) * kHeadDim;
         const uint32_t dst = sQ + (dual ? w * kTileBytes : 0) + (r / 8) * kGroupBytes + (r % 8) * 128;
-        const int c_lo = dual ? 0 : w * 8, c_hi = dual ? 16 : w * 8 + 8;
+        const int nc = dual ? 16 : 8, c_lo = dual ? 0 : w * 8, c_hi = c_lo + nc;
 #pragma unroll 8
         for (int c = c_lo; c < c_hi; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
@@ -719,39 +785,61 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       }
       const bool warp_rows = __any_sync(0xffffffffu, mine);
       float m = -INFINITY, l = 0.f;  // reference (log2 units) and scaled sum
-      bool row_bad = false;
-      const int x0 = dual ? 0 : w, step = dual ? 1 : 2;
-      for (int t = x0; t < g.n && ok; t += step, ++ns) {
-        const int T = T0 + t, kb = g.base + (g.t0 + t) * kTileKeys;
-        ok = __all_sync(0xffffffffu, wait(BAR_SFULL + w, ns));
-        if (!ok) break;
+      float bias = 0.f;              // kShift - m, 0 before the first key
+      const int Y = dual ? 2 * g.n : g.n;
+      // Steps from key wlo to whi need no mask in this warp.
+      const int wlo = __reduce_max_sync(0xffffffffu, mine ? max(lo, g.lo) : g.lo);
+      const int whi = __reduce_min_sync(0xffffffffu, mine ? min(hi, g.hi) : g.hi);
+      const int glo = g.lo, ghi = g.hi, key0 = g.base + g.t0 * kTileKeys;
+      // S of step y: awaited and (its first or second 32 columns) loaded.
+      float va[32], vb[32];
+      auto s_wait = [&](int y) -> bool {
+        const int c = c0 + y;
+        const bool got = __all_sync(0xffffffffu, wait(BAR_SFULL + w * 2 + (c & 1), c >> 1));
         tc_fence_after();
-        // Keys that no row sees must not reach PV: their V rows become 0 (the
-        // converters see to that themselves).
-        if (!kQuant && (kb < g.lo || kb + kTileKeys - 1 > g.hi) && (!dual || w == 0)) {
-          const int st = T % C::VS;
+        return got;
+      };
+      auto s_there = [&](int y) -> bool {
+        const int c = c0 + y;
+        const bool got = __all_sync(0xffffffffu, mbar_test_wait(bar(BAR_SFULL + w * 2 + (c & 1)), (c >> 1) & 1));
+        if (got) tc_fence_after();
+        return got;
+      };
+      auto s_load = [&](int y, int x, float (&v)[32]) {
+        if (warp_rows) tmem_ld32(tmem + lane_off + w * 128 + ((c0 + y) & 1) * kStep + x * 32, v);
+      };
+      bool early = false;  // this step's scores are being loaded already
+      for (int y = 0; y < Y && ok; ++y) {
+        const int T = T0 + (dual ? y >> 1 : y), half = dual ? y & 1 : w, c = c0 + y;
+        const int kb = key0 + (T - T0) * kTileKeys + half * kStep;  // the step's first key
+        const uint32_t tS = tmem + lane_off + w * 128 + (c & 1) * kStep;
+        if (!early) {
+          ok = s_wait(y);
+          if (!ok) break;
+          s_load(y, 0, va);
+          s_load(y, 1, vb);
+        }
+        early = false;
+        // Keys that no row sees must not reach PV: their V rows become 0 (in a
+        // dual segment by both streams, each before its own PV; the converters
+        // see to that themselves).
+        const bool whole = kb >= wlo && kb + kStep - 1 <= whi;  // no row of the warp needs a mask
+        if (!kQuant && !whole && (kb < glo || kb + kStep - 1 > ghi)) {
+          const int st = T % C::VS, key = r % kStep;
           ok = __all_sync(0xffffffffu, wait(BAR_VFULL + st, T / C::VS));
-          if (ok && (kb + r < g.lo || kb + r > g.hi)) {
-            const uint32_t v = sV + st * C::kSlot + (r / 8) * kGroupBytes + (r % 8) * 128;
+          if (ok && (kb + key < glo || kb + key > ghi)) {
+            const int vr = half * kStep + key;
+            const uint32_t v = sV + st * C::kSlot + (vr / 8) * kGroupBytes + (r / kStep) * kAtomBytes +
+                               (vr % 8) * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              sts_v4(v + c * 16, make_uint4(0, 0, 0, 0));
-              sts_v4(v + kAtomBytes + c * 16, make_uint4(0, 0, 0, 0));
-            }
+            for (int x = 0; x < 8; ++x) sts_v4(v + x * 16, make_uint4(0, 0, 0, 0));
           }
           fence_proxy_async_smem();
         }
         if (warp_rows) {
-          const uint32_t badmask = info[T % kInfoSlots];
-          if (badmask != 0) {  // rows that see a chunk of an out-of-range block
-            for (int c = 0; c < kChunksPerTile; ++c)
-              if ((badmask >> (kQuant ? c / 2 * 8 + c % 2 : c) & 1) && kb + c * kChunk <= hi &&
-                  kb + c * kChunk + kChunk - 1 >= lo)
-                row_bad = true;
-          }
-          const bool whole = __all_sync(0xffffffffu, !mine || (lo <= kb && hi >= kb + kTileKeys - 1));
           // int8 rows: the tile's scales of K (times the softmax scale) and V.
-          const float4* ks = reinterpret_cast<const float4*>(smem + C::kScales) + T % kScaleSlots * 32;
+          const float4* ks = reinterpret_cast<const float4*>(smem + C::kScales) + T % kScaleSlots * 32 +
+                             half * (kStep / 4);
           const float4* vs = ks + kScaleSlots * 32;
           // Hidden keys among the 32 from kb + 32 c: -inf in their place.
           auto mask = [&](float (&v)[32], int c) {
@@ -763,198 +851,213 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (!(see >> i & 1)) v[i] = -INFINITY;
           };
-          auto top_of = [&](float (&v)[32], int c) -> float {
+          // int8 rows: the scores times K's row scales, and the power of two
+          // above the step's largest |V scale|.
+          float vtop = 0.f;
+          if constexpr (kRow) {
+            const int st = T % C::VS;
+            ok = __all_sync(0xffffffffu, wait(BAR_VFULL + st, T / C::VS));
+            if (!ok) break;
+            const float2 q2 = *(reinterpret_cast<const float2*>(smem + C::kScales) +
+                                4 * kScaleSlots * 32 + T % kScaleSlots * 2 + half);
+            const float vm = fmaxf(q2.x, q2.y);
+            const int ex = (int)(__float_as_uint(vm) >> 23) - 126;  // vm < 2^ex
+            vtop = (float)min(max(ex, -64), 64);
+          }
+          auto scaled = [&](float (&v)[32], int c) {
             if constexpr (kRow) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const float4 k = ks[c * 8 + e / 4];
-                v[e] *= k.x; v[e + 1] *= k.y; v[e + 2] *= k.z; v[e + 3] *= k.w;
+                const float2 a = mul2(make_float2(v[e], v[e + 1]), make_float2(k.x, k.y));
+                const float2 b = mul2(make_float2(v[e + 2], v[e + 3]), make_float2(k.z, k.w));
+                v[e] = a.x; v[e + 1] = a.y; v[e + 2] = b.x; v[e + 3] = b.y;
               }
             }
             mask(v, c);
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              t0 = fmaxf(t0, fmaxf(v[e], v[e + 1]));
-              t1 = fmaxf(t1, fmaxf(v[e + 2], v[e + 3]));
-            }
-            return fmaxf(t0, t1);
           };
-          // Two passes over S in TMEM (a second read costs less than the 128
-          // registers of a tile's scores), one chunk of 32 keys ahead.
-          float va[32], vb[32];
-          tmem_ld32(tS, va);
-          tmem_ld_wait(va);
-          tmem_ld32(tS + 32, vb);
-          float mx = top_of(va, 0);
-          tmem_ld_wait(vb);
-          tmem_ld32(tS + 64, va);
-          mx = fmaxf(mx, top_of(vb, 1));
-          tmem_ld_wait(va);
-          tmem_ld32(tS + 96, vb);
-          mx = fmaxf(mx, top_of(va, 2));
-          tmem_ld_wait(vb);
-          tmem_ld32(tS, va);
-          mx = fmaxf(mx, top_of(vb, 3));
-          // The reference m: log2 of the largest weight so far and, int8 rows,
-          // of the power of two above the tile's largest |V scale|.
-          float top = kRow ? mx : mx * cs;
-          if constexpr (kRow) {
-            const int st = T % C::VS;
-            ok = __all_sync(0xffffffffu, wait(BAR_VFULL + st, T / C::VS));
-            if (!ok) {
-              tmem_ld_wait();
-              break;
-            }
-            const float4 q4 = *(reinterpret_cast<const float4*>(smem + C::kScales) +
-                                2 * kScaleSlots * 32 + T % kScaleSlots);
-            const float vm = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
-            const int ex = (int)(__float_as_uint(vm) >> 23) - 126;  // vm < 2^ex
-            top += (float)min(max(ex, -64), 64);
-          }
-          tmem_ld_wait(va);
-          const bool raise = top > m + kLazy;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float mn = raise ? top : m;
-            const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-            m = mn;
-            l *= f;
-            if (t != x0) {  // rescale what this stream has accumulated (PV of its last unit is done)
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                float o[32];
-                tmem_ld32(tO + w * 128 + c * 32, o);
-                tmem_ld_wait(o);
+          // Scores to weights, in place; their sum.
+          float2 sum;
+          auto weights = [&](float (&v)[32]) {
+            const float k = kRow ? 1.f : cs;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st<16>(tO + w * 128 + c * 32, o);
-                tmem_st<16, 16>(tO + w * 128 + c * 32 + 16, o);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 z = fma2(make_float2(v[e], v[e + 1]), make_float2(k, k), make_float2(bias, bias));
+              v[e] = fast_exp2(z.x);
+              v[e + 1] = fast_exp2(z.y);
+              sum = add2(sum, make_float2(v[e], v[e + 1]));
+            }
+          };
+          auto all_weights = [&]() -> float {
+            scaled(va, 0);
+            scaled(vb, 1);
+            sum = make_float2(0.f, 0.f);
+            weights(va);
+            weights(vb);
+            return sum.x + sum.y;
+          };
+          tmem_ld_wait(va);
+          tmem_ld_wait(vb);
+          // The weights against the reference so far; a row whose sum (times
+          // the largest |V scale|) stays below the limit keeps it, without its
+          // maximum ever being taken.
+          float total = 0.f;
+          bool need = mine;
+          if (y > 0) {
+            total = all_weights();
+            const float most = kRow ? total * fast_exp2(vtop) : total;
+            need = mine && (m == -INFINITY || !(most <= kSumLimit));
+          }
+          if (__any_sync(0xffffffffu, need)) {
+            // Rows over the limit and rows at their first keys: the reference
+            // becomes the step's maximum; the scores are read again.
+            tmem_ld32(tS, va);
+            tmem_ld32(tS + 32, vb);
+            tmem_ld_wait(va);
+            tmem_ld_wait(vb);
+            scaled(va, 0);
+            scaled(vb, 1);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx = max3(mx, va[e], vb[e]);
+            const float top = (kRow ? mx : mx * cs) + vtop;
+            const float mn = need && top != -INFINITY ? top : m;
+            const bool moved = mn != m;
+            const float f = moved ? fast_exp2(m - mn) : 1.f;
+            m = mn;
+            bias = m == -INFINITY ? 0.f : kShift - m;
+            l *= f;
+            if (y > 0 && __any_sync(0xffffffffu, moved)) {
+              // rescale what this stream has accumulated, once the last step's
+              // PV is done (S of the next step is committed behind it)
+              ok = y + 1 < Y ? s_wait(y + 1) : __all_sync(0xffffffffu, wait(BAR_OFULL + w, seg)) != 0;
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int x = 0; x < 8; ++x) {
+                float o[16];
+                tmem_ld<16>(tO + w * 128 + x * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st<16>(tO + w * 128 + x * 16, o);
               }
               tmem_st_wait();
             }
+            sum = make_float2(0.f, 0.f);
+            weights(va);
+            weights(vb);
+            total = sum.x + sum.y;
           }
-          const float bias = m == -INFINITY ? 0.f : kShift - m;
-          float2 sum = make_float2(0.f, 0.f);
-          // Weights of 32 keys over their scores: 16 columns of high parts,
-          // 16 of residuals.
-          auto weights = [&](float (&v)[32], int c) {
+          l += total;
+          // Weights of 32 keys over their scores: 16 columns of high parts, 16
+          // of residuals (exact: w - fp16(w) fits fp32).
+          auto store = [&](const float (&v)[32], int c) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 k = make_float4(cs, cs, cs, cs);
-              if constexpr (kRow) k = ks[c * 8 + e / 4];
-              const float2 z0 = fma2(make_float2(v[e], v[e + 1]), make_float2(k.x, k.y),
-                                     make_float2(bias, bias));
-              const float2 z1 = fma2(make_float2(v[e + 2], v[e + 3]), make_float2(k.z, k.w),
-                                     make_float2(bias, bias));
-              v[e] = z0.x; v[e + 1] = z0.y; v[e + 2] = z1.x; v[e + 3] = z1.y;
-            }
-            mask(v, c);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int y = 0; y < 2; ++y) {
               uint32_t ph[8], pl[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const int e = 16 * h + 2 * i;
-                float2 x = make_float2(fast_exp2(v[e]), fast_exp2(v[e + 1]));
-                sum = add2(sum, x);
+                const int e = 16 * y + 2 * i;
+                float2 x = make_float2(v[e], v[e + 1]);
                 if constexpr (kRow) x = mul2(x, reinterpret_cast<const float2*>(vs)[c * 16 + e / 2]);
-                // the high part by truncation, so that the residual is exact
-                const float2 hi2 = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u),
-                                               __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
-                const float2 res = add2(x, make_float2(-hi2.x, -hi2.y));
-                ph[i] = h2_bits(__floats2half2_rn(hi2.x, hi2.y));
-                pl[i] = h2_bits(__floats2half2_rn(res.x, res.y));
+                ph[i] = h2_bits(__floats2half2_rn(x.x, x.y));
+                const float2 lo2 = residual(x, ph[i]);
+                pl[i] = h2_bits(__floats2half2_rn(lo2.x, lo2.y));
               }
-              tmem_st8(tS + c * 32 + h * 8, ph);
-              tmem_st8(tS + c * 32 + 16 + h * 8, pl);
+              tmem_st8(tS + c * 32 + y * 8, ph);
+              tmem_st8(tS + c * 32 + 16 + y * 8, pl);
             }
           };
-          tmem_ld32(tS + 32, vb);
-          weights(va, 0);
-          tmem_ld_wait(vb);
-          tmem_ld32(tS + 64, va);
-          weights(vb, 1);
-          tmem_ld_wait(va);
-          tmem_ld32(tS + 96, vb);
-          weights(va, 2);
-          tmem_ld_wait(vb);
-          weights(vb, 3);
-          l += sum.x + sum.y;
+          // Where the next step's scores are there, they are loaded behind this
+          // one's weights.
+          early = y + 1 < Y && s_there(y + 1);
+          store(va, 0);
+          if (early) s_load(y + 1, 0, va);
+          store(vb, 1);
+          if (early) s_load(y + 1, 1, vb);
           tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_PFULL + w));
+        if (lane == 0) mbar_arrive(bar(BAR_PFULL + w * 2 + (c & 1)));
       }
+      if (!ok) tmem_ld_wait();
       // ---- the segment's partial ------------------------------------------------
       ok = __all_sync(0xffffffffu, ok && wait(BAR_SEG, seg));
+      bool row_bad = false;
+      if (*reinterpret_cast<volatile int*>(misc + 9) != 0) {  // rows that see an out-of-range block
+        const int k0 = max(lo, key0), k1 = min(min(hi, ghi), key0 + g.n * kTileKeys - 1);
+        for (int k = k0 / kChunk * kChunk; k <= k1; k += kChunk) {
+          const int phys = __ldg(g.table + k / p.block_size);
+          row_bad |= phys < 0 || phys >= p.num_blocks;
+        }
+      }
       if (threadIdx.x == 0) {
         if (g.flags & kFirst) p.meta[2 + 2 * g.group] = cta;
         if (g.flags & kLast) p.meta[3 + 2 * g.group] = cta;
       }
-      const long long at = g.out_row + local;
-      float* out = p.part_out + at * kHeadDim;
-      if (dual) {
-        if (mine)
-          p.part_lse[at] = (!ok || row_bad || l != l) ? __uint_as_float(kInvalidLse)
-                           : l > 0.f                  ? (m - kShift + log2f(l)) * kLn2
-                                                      : -INFINITY;
-        if (ok && warp_rows) {
-          tc_fence_after();
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+      // Every warpgroup's m and l of its rows, through Q's buffer (it has been read).
+      float2* stat = reinterpret_cast<float2*>(smem + C::kQ);  // [2][128]
+      stat[w * 128 + r] = make_float2(row_bad ? __uint_as_float(kInvalidLse) : m, l);
+      ok = named_bar_and(1, kSoftThreads, ok);
+      const float2 s0 = stat[(dual ? w : 0) * 128 + r];
+      const float2 s1 = dual ? make_float2(-INFINITY, 0.f) : stat[128 + r];
+      named_bar_sync(2, kSoftThreads);
+      // single: the two streams' sums; f0, f1: the accumulators' factors
+      const bool bad = !ok || isnan(s0.x + s0.y) || isnan(s1.x + s1.y);
+      const float mm = fmaxf(s0.x, s1.x);
+      const float w0 = s0.y > 0.f ? fast_exp2(s0.x - mm) : 0.f;
+      const float w1 = s1.y > 0.f ? fast_exp2(s1.x - mm) : 0.f;
+      const float ll = s0.y * w0 + s1.y * w1;
+      if ((dual || w == 0) && mine)
+        p.part_lse[g.out_row + local] = bad        ? __uint_as_float(kInvalidLse)
+                                        : ll > 0.f ? (mm - kShift + log2f(ll)) * kLn2
+                                                   : -INFINITY;
+      if (ok && warp_rows) {
+        tc_fence_after();
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float f0 = w0 * inv, f1 = w1 * inv;
+        const int nx = dual ? 4 : 2, x0 = dual ? 0 : w * 2;  // this warpgroup's chunks of 32 columns
+        const uint32_t stage = sQ + warp * 4096;
+        float* out = p.part_out + (g.out_row + local - lane) * kHeadDim;     // the warp's first row
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld32(tO + w * 128 + c * 32, o);
-            tmem_ld_wait(o);
-            if (mine) {
+        for (int c = x0; c < x0 + nx; ++c) {
+          float o[32];
+          tmem_ld32(tO + (dual ? w * 128 : 0) + c * 32, o);
+          tmem_ld_wait(o);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float4*>(out + c * 32)[e] =
-                    make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+          for (int e = 0; e < 32; ++e) o[e] = f0 > 0.f ? o[e] * f0 : 0.f;  // a stream without keys holds no sums
+          if (!dual) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float o1[16];
+              tmem_ld<16>(tO + 128 + c * 32 + x * 16, o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[x * 16 + e] += f1 > 0.f ? o1[e] * f1 : 0.f;
             }
           }
-        }
-      } else {
-        // Both streams' sums for this row; each warpgroup writes 64 columns.
-        float2* stat = reinterpret_cast<float2*>(smem + C::kQ);  // Q has been read
-        stat[w * 128 + r] = make_float2(row_bad ? __uint_as_float(kInvalidLse) : m, l);
-        ok = named_bar_and(1, 256, ok);
-        const float2 s0 = stat[r], s1 = stat[128 + r];
-        const bool bad = !ok || isnan(s0.x + s0.y) || isnan(s1.x + s1.y);
-        const float mm = fmaxf(s0.x, s1.x);
-        const float w0 = s0.y > 0.f ? fast_exp2(s0.x - mm) : 0.f;
-        const float w1 = s1.y > 0.f ? fast_exp2(s1.x - mm) : 0.f;
-        const float ll = s0.y * w0 + s1.y * w1;
-        if (w == 0 && mine)
-          p.part_lse[at] = bad        ? __uint_as_float(kInvalidLse)
-                           : ll > 0.f ? (mm - kShift + log2f(ll)) * kLn2
-                                      : -INFINITY;
-        if (ok && warp_rows) {
-          tc_fence_after();
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
-          const float f0 = w0 * inv, f1 = w1 * inv;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float o0[32], o1[32];
-            tmem_ld32(tO + w * 64 + c * 32, o0);
-            tmem_ld32(tO + 128 + w * 64 + c * 32, o1);
-            tmem_ld_wait(o0);
-            tmem_ld_wait(o1);
-            if (mine) {
+          // rows to coalesced lines through this warp's 4 KB of the buffer
 #pragma unroll
-              for (int e = 0; e < 32; ++e)  // a stream without keys holds no sums
-                o0[e] = (f0 > 0.f ? o0[e] * f0 : 0.f) + (f1 > 0.f ? o1[e] * f1 : 0.f);
+          for (int e = 0; e < 8; ++e)
+            sts_v4(stage + lane * 128 + ((e ^ (lane % 8)) * 16),
+                   make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                              __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
+          __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float4*>(out + w * 64 + c * 32)[e] =
-                    make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
-            }
+          for (int e = 0; e < 8; ++e) {
+            const int y = e * 4 + lane / 8;  // row of the warp
+            const uint4 u = lds_v4(stage + y * 128 + (((lane % 8) ^ (y % 8)) * 16));
+            if (local - lane + y < g.nrows)
+              *(reinterpret_cast<uint4*>(out + (long long)y * kHeadDim + c * 32) + lane % 8) = u;
           }
+          __syncwarp();
         }
-        named_bar_sync(2, 256);  // the sums have been read: Q may be staged again
       }
+      named_bar_sync(3, kSoftThreads);  // Q may be staged again
       T0 += g.n;
+      c0 += Y;
       ++seg;
     });
   }
