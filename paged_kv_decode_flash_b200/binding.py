@@ -56,6 +56,8 @@ _LIB = None
 def lib() -> ctypes.CDLL:
     """The loaded libpagedattn.so (raises if it has not been built)."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _lock:
         if _LIB is None:
             if not os.path.exists(LIB_PATH):
@@ -127,6 +129,30 @@ def _stream_ptr(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
+
+
+def _on(index: int, stream, call):
+    """call(stream pointer) with device `index` current; stream None: its
+    current one."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return call(_stream_ptr(stream))
+    return call(torch._C._cuda_getCurrentRawStream(index) if stream is None
+                else stream.cuda_stream)
+
+
+def _given(t, name: str, dtype, shape, device) -> int:
+    """The address of a tensor that must be of this type, shape and device,
+    and contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype or t.shape != shape:
+        _expect(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libpagedattn takes contiguous tensors")
+    return t.data_ptr()
 
 
 def _dptr(t: torch.Tensor | None) -> int | None:

@@ -14,6 +14,7 @@
 // (dependent trips to L2 between barriers); the copies are HBM bandwidth.
 // The planning kernels are one thread-block cluster, whose hardware barrier
 // joins the phases without a second launch.
+#include <atomic>
 #include <climits>
 
 #include "common.cuh"
@@ -34,9 +35,9 @@ __device__ __forceinline__ unsigned cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Every thread of the cluster; what was written before is visible after.
+// Every thread of the cluster; what was written before is visible after (to
+// the cluster's threads: the barrier releases and acquires).
 __device__ __forceinline__ void cluster_sync() {
-  __threadfence();
   asm volatile(
       "barrier.cluster.arrive.release;\n\t"
       "barrier.cluster.wait.acquire;" ::
@@ -96,13 +97,15 @@ __device__ __forceinline__ void pool_share(int num_blocks, int rank, int& b0, in
 // One CTA per request.  A request stands unless a row is out of range, the
 // child has tokens, an earlier request has the same child, or the parent is
 // a child of the call itself (its row is being written).
-__global__ void __launch_bounds__(256) fork_kernel(const PageParams p) {
+constexpr int kForkThreads = 256;
+
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const PageParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x, tid = threadIdx.x;
   const int par = __ldg(p.parents + i), child = __ldg(p.rows + i);
   bool bad = !row_ok(p, par) || !row_ok(p, child);
-  for (int j = tid; j < p.n; j += blockDim.x) {
+  for (int j = tid; j < p.n; j += kForkThreads) {
     const int c = __ldg(p.rows + j);
     bad |= c == par || (c == child && j < i);
   }
@@ -124,13 +127,31 @@ __global__ void __launch_bounds__(256) fork_kernel(const PageParams p) {
   const int held = pages_of(p, L);
   const int32_t* from = table_row(p, par);
   int32_t* to = table_row(p, child);
+  // The first pages stay in registers between the check and the copy.
+  constexpr int kKeep = 4;
+  int kept[kKeep];
   bool bad_page = false;
-  for (int b = tid; b < held; b += blockDim.x) bad_page |= !page_ok(p, __ldcg(from + b));
+#pragma unroll
+  for (int e = 0; e < kKeep; ++e) {
+    const int b = tid + e * kForkThreads;
+    kept[e] = b < held ? __ldcg(from + b) : 0;
+  }
+#pragma unroll
+  for (int e = 0; e < kKeep; ++e) bad_page |= !page_ok(p, kept[e]);
+  for (int b = tid + kKeep * kForkThreads; b < held; b += kForkThreads) bad_page |= !page_ok(p, __ldcg(from + b));
   if (__syncthreads_or(bad_page)) {
     if (tid == 0) atomicOr(p.flags, kFlagBadBlock);
     return;
   }
-  for (int b = tid; b < held; b += blockDim.x) {
+#pragma unroll
+  for (int e = 0; e < kKeep; ++e) {
+    const int b = tid + e * kForkThreads;
+    if (b < held) {
+      to[b] = kept[e];
+      atomicAdd(p.ref_counts + kept[e], 1);
+    }
+  }
+  for (int b = tid + kKeep * kForkThreads; b < held; b += kForkThreads) {
     const int page = __ldcg(from + b);
     to[b] = page;
     atomicAdd(p.ref_counts + page, 1);
@@ -143,7 +164,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const PageParams p) {
 // a row; holders[page] and keeper[page] how many requests grow out of the
 // ragged page and the last of them; need[i] / end[i] fresh pages of request
 // i and their running total; fresh[k] the k-th lowest free page.
-enum : int { kStands = 1, kGrows = 2, kSplits = 4 };
+enum : int { kStands = 1, kGrows = 2 };
 
 __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PageParams p) {
   __shared__ int sums[32];
@@ -323,6 +344,217 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PageParam
   }
 }
 
+// The same for at most kOneRequests requests on at most kOnePages pages, with
+// one cluster barrier: every CTA makes the whole plan by itself (a request and
+// 32 pages a thread; the requests are compared in shared memory), and after
+// the barrier, when all have read the books, each changes its share of the
+// table entries and counts.  Bound: the chain of dependent trips to L2
+// (request, length, page, count; entry, count); the other form's phases cost a
+// fence, a cluster barrier and a trip each.
+constexpr int kOneRequests = kPlanThreads, kOnePages = 32 * kPlanThreads;
+constexpr int kPiece = 256;      // table entries a warp changes at a time
+constexpr int kOneFresh = 8192;  // fresh pages listed in shared memory
+
+__global__ void __launch_bounds__(kPlanThreads, 1) resize_one_kernel(const PageParams p) {
+  __shared__ int sums[32];
+  __shared__ long long long_sums[32];
+  __shared__ uint16_t near_list[kOneFresh];
+  __shared__ int last_piece[kOneRequests];
+  __shared__ __align__(16) int at_row[kOneRequests], at_page[kOneRequests];
+  __shared__ int at_fresh[kOneRequests], at_count[kOneRequests];
+  extern __shared__ int given_up[];  // [num_blocks]
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rank = (int)cluster_rank(), i = threadIdx.x, lane = i % 32, warp = i / 32;
+  const bool mine = i < p.n;
+  const int row = mine ? __ldg(p.rows + i) : -1;
+  const int want = mine && p.new_lens != nullptr ? __ldg(p.new_lens + i) : 0;
+  int L = mine && row_ok(p, row) ? __ldcg(p.context_lens + row) : 0;
+  // Pages 32 i .. 32 i + 31: bit set = free.
+  uint32_t free_mask = 0;
+  {
+    int c[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const int b = (warp * 32 + k) * 32 + lane;
+      c[k] = b < p.num_blocks ? __ldcg(p.ref_counts + b) : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const uint32_t m = __ballot_sync(0xffffffffu, c[k] == 0);
+      if (lane == k) free_mask = m;
+    }
+  }
+  // ---- the request on its own
+  unsigned flags = 0;
+  bool stands = false, grows = false;
+  int page = -1;
+  if (mine) {
+    stands = row_ok(p, row);
+    if (!stands) {
+      flags = kFlagBadRequest;
+      L = 0;
+    } else if (!len_ok(p, want) || !len_ok(p, L)) {
+      flags = kFlagBadLen;
+      stands = false;
+    } else if (want > L) {
+      grows = true;
+      if (L % p.block_size != 0) {
+        page = __ldcg(table_row(p, row) + L / p.block_size);
+        if (!page_ok(p, page)) {
+          flags = kFlagBadBlock;
+          stands = false;
+        }
+      }
+    }
+  }
+  // ---- among the others: the first of its row; who grows out of a page
+  at_row[i] = stands ? row : -1;
+  __syncthreads();
+  const int n4 = (p.n + 3) / 4;
+  if (stands) {
+    int lowest = i;
+#pragma unroll 8
+    for (int j = n4 - 1; j >= 0; --j) {
+      const int4 r = reinterpret_cast<const int4*>(at_row)[j];
+      if (r.w == row) lowest = min(lowest, 4 * j + 3);
+      if (r.z == row) lowest = min(lowest, 4 * j + 2);
+      if (r.y == row) lowest = min(lowest, 4 * j + 1);
+      if (r.x == row) lowest = min(lowest, 4 * j);
+    }
+    if (lowest != i) {
+      flags = kFlagBadRequest;
+      stands = false;
+    }
+  }
+  const bool ragged = stands && grows && page >= 0;
+  const int refs = ragged ? __ldcg(p.ref_counts + page) : 0;
+  at_page[i] = ragged ? page : -1;
+  __syncthreads();
+  bool split = refs > 1;
+  if (split) {
+    int holders = 0, keeper = 0;
+#pragma unroll 8
+    for (int j = 0; j < n4; ++j) {
+      const int4 q = reinterpret_cast<const int4*>(at_page)[j];
+      holders += (q.x == page) + (q.y == page) + (q.z == page) + (q.w == page);
+      if (q.x == page) keeper = max(keeper, 4 * j);
+      if (q.y == page) keeper = max(keeper, 4 * j + 1);
+      if (q.z == page) keeper = max(keeper, 4 * j + 2);
+      if (q.w == page) keeper = max(keeper, 4 * j + 3);
+    }
+    split = !(holders == refs && keeper == i);
+  }
+  // ---- fresh pages: the lowest free ones in the order of the requests
+  const int have = pages_of(p, L), wanted = pages_of(p, want);
+  const long long need = stands && grows ? (long long)wanted - have + split : 0;
+  // Both running totals in one: the needs, which may add up past 32 bits, and
+  // in the low 20 bits the free pages.
+  const long long both = need << 20 | __popc(free_mask);
+  long long all;
+  const long long before = block_scan(both, long_sums, all);
+  const long long all_need = all >> 20, end = (before >> 20) + need;
+  const int nfree = (int)(all & 0xfffff);
+  int k = (int)(before & 0xfffff);
+  const int listed = (int)min(all_need, (long long)nfree);
+  const bool near = listed <= kOneFresh;
+  int* far_list = p.page_scratch + 2LL * p.num_blocks;
+  for (uint32_t m = free_mask; m != 0 && k < listed; m &= m - 1, ++k) {
+    const int b = 32 * i + __ffs(m) - 1;
+    if (near) near_list[k] = (uint16_t)b;
+    else if (rank == 0) far_list[k] = b;
+  }
+  if (stands && grows && end > nfree) {
+    flags = kFlagNoPages;
+    stands = false;
+  }
+  const int change = stands ? wanted - have : 0;  // entries taken, or (negative) given up
+  // Pieces of kPiece entries; last_piece: their running total.
+  int pieces;
+  last_piece[i] = block_scan((abs(change) + kPiece - 1) / kPiece, sums, pieces) +
+                  (abs(change) + kPiece - 1) / kPiece;
+  at_count[i] = change;
+  at_row[i] = row;
+  at_page[i] = grows ? have : wanted;
+  at_fresh[i] = (int)(end - change);
+  cluster_sync();  // the books have been read
+  auto fresh = [&](int x) { return near ? (int)near_list[x] : __ldcg(far_list + x); };
+  if (mine && rank == 0) {
+    int src = -1, dst = -1;
+    if (stands) {
+      if (split) {
+        src = page;
+        dst = fresh((int)(end - need));
+        table_row(p, row)[L / p.block_size] = dst;
+        p.ref_counts[dst] = 1;
+        atomicSub(p.ref_counts + page, 1);
+      }
+      p.context_lens[row] = want;
+    }
+    p.copy_src[i] = src;
+    p.copy_dst[i] = dst;
+  }
+  if (rank != 0) flags = 0;
+  const bool drops = __syncthreads_or(change < 0);
+  if (drops) {
+    for (int b = i; b < p.num_blocks; b += kPlanThreads) given_up[b] = 0;
+    __syncthreads();
+  }
+  // This CTA's run of the pieces, a warp each.
+  const int q1 = (int)((long long)pieces * (rank + 1) / kPlanCtas);
+  for (int q = (int)((long long)pieces * rank / kPlanCtas) + warp; q < q1; q += kPlanThreads / 32) {
+    int lo = 0, hi = p.n - 1;  // the first request with last_piece > q
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (last_piece[mid] > q) hi = mid;
+      else lo = mid + 1;
+    }
+    const int o0 = (q - (lo > 0 ? last_piece[lo - 1] : 0)) * kPiece, count = at_count[lo];
+    int32_t* entry = table_row(p, at_row[lo]) + at_page[lo] + o0 + lane;
+    const int left = abs(count) - o0 - lane;  // this lane's entries: 0, 32, .. below it
+    if (count > 0) {
+#pragma unroll
+      for (int e = 0; e < kPiece; e += 32) {
+        if (e >= left) continue;
+        const int pg = fresh(at_fresh[lo] + o0 + lane + e);
+        entry[e] = pg;
+        p.ref_counts[pg] = 1;
+      }
+    } else {
+      int pg[kPiece / 32];
+#pragma unroll
+      for (int e = 0; e < kPiece; e += 32) pg[e / 32] = e < left ? __ldcg(entry + e) : 0;
+#pragma unroll
+      for (int e = 0; e < kPiece; e += 32) {
+        if (e >= left) continue;
+        if (page_ok(p, pg[e / 32])) atomicAdd(given_up + pg[e / 32], 1);
+        else flags |= kFlagBadBlock;
+      }
+    }
+  }
+  if (drops) {  // (the same in every CTA)
+    // Given-up pages are counted in shared memory first: they lie anywhere, and
+    // a GPC's atomics on single words of L2 are slow (63,000 of them: 40 us).
+    __syncthreads();
+#pragma unroll 8
+    for (int b = i; b < p.num_blocks; b += kPlanThreads)
+      if (given_up[b] != 0) atomicSub(p.ref_counts + b, given_up[b]);
+    cluster_sync();
+    bool wrong = false;
+#pragma unroll 8
+    for (int b = i; b < p.num_blocks; b += kPlanThreads) {
+      const int c = __ldcg(p.ref_counts + b);
+      wrong |= c < 0 && given_up[b] != 0;
+    }
+    if (wrong) {  // pages that were not held: the books were wrong
+      flags |= kFlagBadRequest;
+      for (int b = i; b < p.num_blocks; b += kPlanThreads)
+        if (given_up[b] != 0) atomicMax(p.ref_counts + b, 0);
+    }
+  }
+  if (flags != 0) atomicOr(p.flags, flags);
+}
+
 // ---------------------------------------------------------------- compact
 // n_live live pages; the k-th lowest live page at or above n_live moves to
 // the k-th lowest free page below it.
@@ -448,8 +680,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) copy_check_kernel(const PageP
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;                                  // 16-byte vectors per thread
 constexpr int kCopyPiece = kCopyThreads * kCopyVecs * 16;     // bytes per work unit
+// Up to this many pairs every CTA looks its own ones over against the list
+// (eight entries a thread): no launch and no cluster barriers before the
+// copies, 5.1 us instead of 6.1 for 7 pairs (with host time 10 instead of 16).
+constexpr int kCopySelfCheck = 2048;
 
 // Persistent: units (pair, K or V, piece of a page) over the grid.
+template <bool kCheck>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PageParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -457,11 +694,33 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PageParams p) 
   const int n = p.count != nullptr ? max(0, min(p.n, __ldcg(p.count))) : p.n;
   const int pieces = (int)((p.page_bytes + kCopyPiece - 1) / kCopyPiece);
   const long long units = (long long)n * 2 * pieces;
+  int seen = -1, s = -1, d = -1;  // the pair that was looked over last
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int i = (int)(u / (2 * pieces)), r = (int)(u % (2 * pieces));
-    const int s = __ldcg(src_ok + i);
+    if (!kCheck) {
+      s = __ldcg(src_ok + i);
+      d = __ldcg(p.copy_dst + i);
+    } else if (i != seen) {
+      seen = i;
+      s = __ldcg(p.copy_src + i);
+      d = __ldcg(p.copy_dst + i);
+      if (s >= 0) {
+        unsigned bad = page_ok(p, s) && page_ok(p, d) ? 0u : kFlagBadBlock;
+        if (bad == 0) {
+          bool clash = false;
+          for (int j = threadIdx.x; j < n; j += kCopyThreads) {
+            const int sj = __ldcg(p.copy_src + j), dj = __ldcg(p.copy_dst + j);
+            if (sj >= 0 && page_ok(p, sj) && page_ok(p, dj)) clash |= dj == s || (dj == d && j < i);
+          }
+          if (__syncthreads_or(clash)) bad = kFlagBadRequest;
+        }
+        if (bad != 0) {
+          if (threadIdx.x == 0) atomicOr(p.flags, bad);
+          s = -1;
+        }
+      }
+    }
     if (s < 0) continue;
-    const int d = __ldcg(p.copy_dst + i);
     uint8_t* base = static_cast<uint8_t*>(r < pieces ? p.k_cache : p.v_cache);
     const long long off = (long long)(r % pieces) * kCopyPiece + threadIdx.x * 16;
     const uint4* from = reinterpret_cast<const uint4*>(base + s * p.page_bytes + off);
@@ -477,8 +736,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PageParams p) 
 }
 
 cudaError_t launch(void (*kern)(const PageParams), unsigned grid, unsigned threads, int cluster,
-                   const PageParams& p, cudaStream_t stream) {
+                   const PageParams& p, cudaStream_t stream, size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
@@ -497,9 +757,24 @@ cudaError_t launch(void (*kern)(const PageParams), unsigned grid, unsigned threa
 }  // namespace
 
 cudaError_t launch_fork(const PageParams& p, cudaStream_t stream) {
-  return launch(fork_kernel, p.n, 256, 1, p, stream);
+  return launch(fork_kernel, p.n, kForkThreads, 1, p, stream);
 }
 cudaError_t launch_resize(const PageParams& p, cudaStream_t stream) {
+  if (p.n <= kOneRequests && p.num_blocks <= kOnePages) {
+    static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+      e = cudaFuncSetAttribute(resize_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kOnePages * (int)sizeof(int));
+      if (e != cudaSuccess) return e;
+      ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    return launch(resize_one_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream,
+                  p.num_blocks * sizeof(int));
+  }
   return launch(resize_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
 }
 cudaError_t launch_compact(const PageParams& p, cudaStream_t stream) {
@@ -508,11 +783,13 @@ cudaError_t launch_compact(const PageParams& p, cudaStream_t stream) {
   return launch(remap_kernel, p.num_seqs, 256, 1, p, stream);
 }
 cudaError_t launch_copy_blocks(const PageParams& p, int sms, cudaStream_t stream) {
-  const cudaError_t e = launch(copy_check_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
-  if (e != cudaSuccess) return e;
   const long long units = (long long)p.n * 2 * ((p.page_bytes + kCopyPiece - 1) / kCopyPiece);
   const long long most = (long long)sms * 8;
-  return launch(copy_kernel, (unsigned)(units < most ? units : most), kCopyThreads, 1, p, stream);
+  const unsigned grid = (unsigned)(units < most ? units : most);
+  if (p.n <= kCopySelfCheck) return launch(copy_kernel<true>, grid, kCopyThreads, 1, p, stream);
+  const cudaError_t e = launch(copy_check_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
+  if (e != cudaSuccess) return e;
+  return launch(copy_kernel<false>, grid, kCopyThreads, 1, p, stream);
 }
 
 }  // namespace pa

@@ -69,47 +69,44 @@ class PagePool:
                       "pages_workspace_init")
 
     def _given(self, t, name, shape):
-        _b._expect(t, name, torch.int32, shape)
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the pool on {self.device}")
-        return _b._dptr(t)
+        return _b._given(t, name, torch.int32, shape, self.device)
 
     def _books(self):
         return (self.block_table.data_ptr(), self.context_lens.data_ptr(),
                 self.ref_counts.data_ptr())
 
-    def _new(self, n, stream):
-        t = torch.empty(n, dtype=torch.int32, device=self.device)
+    def _new(self, sizes, stream):
+        """int32 tensors of these sizes, in one allocation."""
+        t = torch.empty(sum(sizes), dtype=torch.int32, device=self.device)
         if stream is not None:
             t.record_stream(stream)
-        return t
+        return t.split(sizes)
 
     def fork(self, parents, children, *, stream=None) -> None:
         """paged_attn_fork: the empty rows ``children`` become copies of the
         rows ``parents`` and hold the same pages."""
-        n = int(children.numel())
+        n = children.numel()
         pp = self._given(parents, "parents", (n,))
         cp = self._given(children, "children", (n,))
-        with torch.cuda.device(self.device):
-            rc = _b.lib().paged_attn_fork(ctypes.byref(self.dims), *self._books(), pp, cp, n,
-                                          _b._stream_ptr(stream))
-        _b._check(rc, "paged_attn_fork")
+        _b._check(_b._on(self.device.index, stream, lambda st: _b.lib().paged_attn_fork(
+            self.dims, *self._books(), pp, cp, n, st)), "paged_attn_fork")
 
     def resize(self, rows, new_lens=None, *, copy_src=None, copy_dst=None, stream=None):
         """paged_attn_resize: ``rows`` get the lengths ``new_lens`` (None: 0).
         Returns (src, dst) int32 [n]: the pages to copy (-1: none) on every
         layer before the new tokens are written."""
-        n = int(rows.numel())
+        n = rows.numel()
         rp = self._given(rows, "rows", (n,))
         lp = None if new_lens is None else self._given(new_lens, "new_lens", (n,))
-        with torch.cuda.device(self.device):
-            src = self._new(n, stream) if copy_src is None else copy_src
-            dst = self._new(n, stream) if copy_dst is None else copy_dst
-            rc = _b.lib().paged_attn_resize(
-                ctypes.byref(self.dims), *self._books(), rp, lp, n,
-                self._given(src, "copy_src", (n,)), self._given(dst, "copy_dst", (n,)),
-                _b._stream_ptr(stream))
-        _b._check(rc, "paged_attn_resize")
+        if copy_src is None or copy_dst is None:
+            src, dst = self._new((n, n), stream)
+            sp, dp = src.data_ptr(), dst.data_ptr()
+        if copy_src is not None:
+            src, sp = copy_src, self._given(copy_src, "copy_src", (n,))
+        if copy_dst is not None:
+            dst, dp = copy_dst, self._given(copy_dst, "copy_dst", (n,))
+        _b._check(_b._on(self.device.index, stream, lambda st: _b.lib().paged_attn_resize(
+            self.dims, *self._books(), rp, lp, n, sp, dp, st)), "paged_attn_resize")
         return src, dst
 
     def free(self, rows, *, stream=None) -> None:
@@ -120,34 +117,26 @@ class PagePool:
         """paged_attn_compact: the live pages become the first ones of the
         pool.  Returns the moves, to be copied on every layer."""
         room = max(1, self.dims.num_blocks // 2)
-        with torch.cuda.device(self.device):
-            m = Moves(self._new(room, stream), self._new(room, stream), self._new(1, stream),
-                      self._new(self.dims.num_blocks, stream))
-            rc = _b.lib().paged_attn_compact(
-                ctypes.byref(self.dims), *self._books(), _b._dptr(m.src), _b._dptr(m.dst),
-                _b._dptr(m.count), _b._dptr(m.remap), _b._stream_ptr(stream))
-        _b._check(rc, "paged_attn_compact")
+        m = Moves(*self._new((room, room, 1, self.dims.num_blocks), stream))
+        _b._check(_b._on(self.device.index, stream, lambda st: _b.lib().paged_attn_compact(
+            self.dims, *self._books(), m.src.data_ptr(), m.dst.data_ptr(), m.count.data_ptr(),
+            m.remap.data_ptr(), st)), "paged_attn_compact")
         return m
 
     def copy(self, k_cache, v_cache, src, dst, *, kv_dtype: int, count=None, stream=None) -> None:
         """paged_attn_copy_blocks on one layer's caches: page dst[i] becomes a
         copy of page src[i] (negative src: skipped)."""
         d = self.dims
-        shape = _b.cache_shape(kv_dtype, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            _b._expect(t, name, *shape)
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the pool on {self.device}")
-        n = int(src.numel())
+        dtype, shape = _b.cache_shape(kv_dtype, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+        kp = _b._given(k_cache, "k_cache", dtype, shape, self.device)
+        vp = _b._given(v_cache, "v_cache", dtype, shape, self.device)
+        n = src.numel()
         sp, dp = self._given(src, "src", (n,)), self._given(dst, "dst", (n,))
         cp = None if count is None else self._given(count, "count", (1,))
-        with torch.cuda.device(self.device):
-            rc = _b.lib().paged_attn_copy_blocks(
-                ctypes.byref(d), sp, dp, n, cp, int(kv_dtype), _b._dptr(k_cache),
-                _b._dptr(v_cache), _b._stream_ptr(stream))
-        _b._check(rc, "paged_attn_copy_blocks")
+        _b._check(_b._on(self.device.index, stream, lambda st: _b.lib().paged_attn_copy_blocks(
+            d, sp, dp, n, cp, int(kv_dtype), kp, vp, st)), "paged_attn_copy_blocks")
 
     def get_error(self, stream=None) -> int:
         """Synchronises and returns (and clears) what the device refused."""
-        with torch.cuda.device(self.device):
-            return _b.lib().paged_attn_get_error(ctypes.byref(self.dims), _b._stream_ptr(stream))
+        return _b._on(self.device.index, stream,
+                      lambda st: _b.lib().paged_attn_get_error(self.dims, st))

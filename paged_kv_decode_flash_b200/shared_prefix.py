@@ -48,12 +48,10 @@ class SharedPrefixDecode(_b.PagedDecode):
                    device=device)
 
     def check_shared(self, prefix_table, prefix_len):
-        _b._expect(prefix_table, "prefix_table", torch.int32, (self.prefix_blocks,))
-        _b._expect(prefix_len, "prefix_len", torch.int32, (1,))
-        for name, t in (("prefix_table", prefix_table), ("prefix_len", prefix_len)):
-            if t.device != self.workspace.device:
-                raise ValueError(f"{name} is on {t.device}, the workspace on "
-                                 f"{self.workspace.device}")
+        """The addresses of the prefix's tensors, checked."""
+        dev = self.workspace.device
+        return (_b._given(prefix_table, "prefix_table", torch.int32, (self.prefix_blocks,), dev),
+                _b._given(prefix_len, "prefix_len", torch.int32, (1,), dev))
 
     def __call__(self, q, k_cache, v_cache, block_table, context_lens, prefix_table=None,
                  prefix_len=None, *, causal: int, window: int, scale: float, kv_dtype: int,
@@ -65,17 +63,22 @@ class SharedPrefixDecode(_b.PagedDecode):
             return super().__call__(q, k_cache, v_cache, block_table, context_lens, causal=causal,
                                     window=window, scale=scale, kv_dtype=kv_dtype, out=out,
                                     stream=stream)
-        self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
-        self.check_shared(prefix_table, prefix_len)
-        with torch.cuda.device(self.workspace.device):
-            if out is None:
-                out = torch.empty_like(q)
-                if stream is not None:
-                    out.record_stream(stream)
-            rc = _b.lib().paged_attn_decode_shared(
-                ctypes.byref(self.dims), _b._dptr(q), _b._dptr(k_cache), _b._dptr(v_cache),
-                _b._dptr(block_table), _b._dptr(context_lens), _b._dptr(prefix_table),
-                _b._dptr(prefix_len), self.prefix_blocks, self.n_query, int(causal), int(window),
-                float(scale), int(kv_dtype), _b._dptr(out), _b._stream_ptr(stream))
-        _b._check(rc, "paged_attn_decode_shared")
+        d, dev = self.dims, self.workspace.device
+        qshape = (d.num_seqs, self.n_query, d.num_q_heads, d.head_dim)
+        dtype, shape = _b.cache_shape(kv_dtype, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+        args = (_b._given(q, "q", torch.float16, qshape, dev),
+                _b._given(k_cache, "k_cache", dtype, shape, dev),
+                _b._given(v_cache, "v_cache", dtype, shape, dev),
+                _b._given(block_table, "block_table", torch.int32,
+                          (d.num_seqs, d.max_blocks_per_seq), dev),
+                _b._given(context_lens, "context_lens", torch.int32, (d.num_seqs,), dev),
+                *self.check_shared(prefix_table, prefix_len))
+        if out is None:
+            out = torch.empty_like(q)
+            if stream is not None:
+                out.record_stream(stream)
+        op = _b._given(out, "out", torch.float16, qshape, dev)
+        _b._check(_b._on(dev.index, stream, lambda st: _b.lib().paged_attn_decode_shared(
+            d, *args, self.prefix_blocks, self.n_query, int(causal), int(window), float(scale),
+            int(kv_dtype), op, st)), "paged_attn_decode_shared")
         return out
