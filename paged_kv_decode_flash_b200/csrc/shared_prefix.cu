@@ -18,6 +18,8 @@ namespace {
 
 using namespace sm100;
 
+constexpr int kJoin = 8;  // partials loaded at a time
+
 // The join: one warp per output row over the row's partials, weights
 // e^(lse - max).  A NaN log-sum-exp (an out-of-range block, a timeout) and a
 // bad length give a row of zeros.
@@ -31,10 +33,12 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
   const int NT = (p.rows_head + p.row_tile - 1) / p.row_tile;
   const int rs = rh - s * p.rows_seq, part = rs / p.rows_part;
   const int gp = kvh * NT + rh / p.row_tile, go = s * p.num_kv_heads * p.parts + kvh * p.parts + part;
+  if (row >= rows) return;
+  // (complete since before the other kernel began: that waited for them, too)
+  const int P = __ldg(p.prefix_len), L = __ldg(p.context_lens + s);
   griddep_wait();
   griddep_launch_dependents();
-  if (row >= rows) return;
-  const int P = __ldg(p.prefix_len), L = __ldg(p.context_lens + s), nt = __ldcg(p.meta);
+  const int nt = __ldcg(p.meta);
   const int2 cp = __ldcg(reinterpret_cast<const int2*>(p.meta) + 1 + gp);
   const int2 co = __ldcg(reinterpret_cast<const int2*>(p.meta) + 1 + p.num_kv_heads * NT + go);
   bool ok = shared_prefix_ok(p, P);
@@ -61,27 +65,36 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
   for (int k0 = 0; k0 < np + no; k0 += 32) {  // 32 partials at a time, lane k their lse
     const int n = min(32, np + no - k0);
     const float e = lane < n ? __ldcg(p.part_lse + slot(k0 + lane)) : -INFINITY;
-    bad |= __any_sync(0xffffffffu, isnan(e));
-    float mx = fmaxf(e, M);
+    float mx = 0.f, we = 0.f;
+    for (int k = 0; k < n; k += kJoin) {  // the first ones are loaded beside the lse
+      float4 v[kJoin];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    if (mx == -INFINITY) continue;
-    const float f = expf(M - mx), we = expf(e - mx);
-    M = mx;
-    l *= f;
+      for (int x = 0; x < kJoin; ++x)
+        v[x] = k + x < n ? __ldcg(reinterpret_cast<const float4*>(p.part_out + slot(k0 + k + x) * kHeadDim) + lane)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k == 0) {
+        bad |= __any_sync(0xffffffffu, isnan(e));
+        mx = fmaxf(e, M);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] *= f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, we, k);
-      const float4 v =
-          __ldcg(reinterpret_cast<const float4*>(p.part_out + slot(k0 + k) * kHeadDim) + lane);
-      if (w == 0.f) continue;  // (a partial without keys)
-      l += w;
-      o[0] = fmaf(w, v.x, o[0]);
-      o[1] = fmaf(w, v.y, o[1]);
-      o[2] = fmaf(w, v.z, o[2]);
-      o[3] = fmaf(w, v.w, o[3]);
+        for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        if (mx == -INFINITY) break;
+        const float f = expf(M - mx);
+        we = expf(e - mx);
+        M = mx;
+        l *= f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] *= f;
+      }
+#pragma unroll
+      for (int x = 0; x < kJoin; ++x) {
+        const float w = __shfl_sync(0xffffffffu, we, (k + x) & 31);
+        if (k + x >= n || w == 0.f) continue;  // (0: a partial without keys)
+        l += w;
+        o[0] = fmaf(w, v[x].x, o[0]);
+        o[1] = fmaf(w, v[x].y, o[1]);
+        o[2] = fmaf(w, v[x].z, o[2]);
+        o[3] = fmaf(w, v[x].w, o[3]);
+      }
     }
   }
   const float inv = l > 0.f && !bad ? 1.f / l : 0.f;

@@ -78,7 +78,7 @@ constexpr float kSumLimit = 32768.f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kInvalidLse = 0x7fc00000u;  // NaN: a partial that must not be used
 constexpr int kStep = 64;       // keys of a step of a stream
-constexpr int kOwnStart = 4;    // what the start of an own-keys segment costs, in units
+constexpr int kOwnStart = 3;    // what the start of an own-keys segment costs, in units
 constexpr int kScaleSlots = 8;  // tiles whose row scales are kept: more than are in flight
 
 constexpr int kSegSlots = 4;
@@ -96,7 +96,8 @@ enum : int {
   BAR_DONE = 24,
   BAR_GFULL = 25,  // [kSegSlots] a segment's description published
   BAR_GEMPTY = 29, // [kSegSlots] ... read by every role
-  BAR_COUNT = 33
+  BAR_OEMPTY = 33, // a segment's O accumulators read
+  BAR_COUNT = 34
 };
 
 template <int KV>
@@ -114,7 +115,7 @@ struct Cfg {
   static constexpr uint32_t kK = kQ + (kQuant ? 1 : 2) * kTileBytes;
   static constexpr uint32_t kV = kK + KS * kSlot;
   static constexpr uint32_t kBars = kV + VS * kSlot;
-  static constexpr uint32_t kMisc = kBars + BAR_COUNT * 8 + 8;         // int [16], see below
+  static constexpr uint32_t kMisc = kBars + (BAR_COUNT * 8 + 15) / 16 * 16;         // int [16], see below
   static constexpr uint32_t kSegs = kMisc + 64;             // Segment [kSegSlots]
   static constexpr uint32_t kScales = kSegs + kSegSlots * 64;  // int8 rows: float K [8][128], V [8][128], max [8][4]
   static constexpr uint32_t kTotal = kScales + (kRow ? kScaleSlots * (2 * 128 + 4) * 4 : 0);
@@ -190,6 +191,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// a / b for a >= 0, b > 0, mostly in 32 bits.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Tiles of a set of keys [lo, hi]: from `base` (lo rounded down to a chunk).
 __device__ __forceinline__ int key_tiles(int lo, int hi) {
   return hi >= lo ? (hi - lo / kChunk * kChunk) / kTileKeys + 1 : 0;
@@ -206,7 +211,8 @@ struct Segment {
   int group, flags;       // kDual, kFirst, kLast
 };
 static_assert(sizeof(Segment) == 64, "Segment layout");
-enum : int { kDual = 1, kFirst = 2, kLast = 4 };  // more than 128 rows; of the group's segments
+// kDual: more than 128 rows; kFirst, kLast: of the group's segments; kBuf: Q in the second buffer
+enum : int { kDual = 1, kFirst = 2, kLast = 4, kBuf = 8 };
 
 template <int KV>
 __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + C::kQ, sK = sbase + C::kK, sV = sbase + C::kV;
     // [0] TMEM base, [1] abort, [2] shortest sequence, [3] start sequence,
-  // [4, 5] its start, [6, 7] own units of the batch, [8] segments given up,
+  // [4, 5] its start, [6, 7] own tiles and sequences behind the first round, [8] segments given up,
   // [9] a block was out of range
   int* misc = reinterpret_cast<int*>(smem + C::kMisc);
   volatile int* abort = misc + 1;
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < BAR_COUNT; ++i)
-      mbar_init(bar(i), i == BAR_QFULL                                                   ? 8
+      mbar_init(bar(i), i == BAR_QFULL || i == BAR_OEMPTY                                ? 8
                         : (i >= BAR_PFULL && i < BAR_OFULL)                              ? 4
                         : (i < BAR_SFULL && (i % 6 >= 3 || kQuant)) ? (i % 6 >= 3 ? 2 : 4)  // empty, full
                         : i == BAR_SEG || i == BAR_DONE                                  ? 2
@@ -255,6 +261,8 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
   const int P = __ldg(p.prefix_len);
+  const int own_s = threadIdx.x;  // this thread's sequence of the first round
+  const int own_L = own_s < p.num_seqs ? __ldg(p.context_lens + own_s) : 0;
   const bool prefix_ok = shared_prefix_ok(p, P);
   __syncthreads();
 
@@ -272,32 +280,49 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     }
   };
   const int hp = p.num_kv_heads * p.parts;  // own groups of a sequence
-  auto own_units = [&](int L) -> long long {
+  auto own_tiles = [&](int L) -> int {
     int lo, hi;
     own_keys(L, lo, hi);
-    const int t = key_tiles(lo, hi);
-    return t > 0 ? (long long)hp * (t + kOwnStart) : 0;
+    return key_tiles(lo, hi);
   };
+  // Of the batch: the shortest sequence, the sequences with keys of their own,
+  // their tiles; tiles before this thread's sequence among the first round's.
+  long long* sums = reinterpret_cast<long long*>(smem + C::kK);  // [2][warps], no copy is in flight yet
+  const int own_t = own_tiles(own_L);
+  long long ahead = ((long long)own_t << 22) + (own_t > 0);  // tiles, sequences
   {
-    int m = INT32_MAX;
-    long long u = 0;
-    for (int s = threadIdx.x; s < p.num_seqs; s += C::kThreads) {
+    int m = prefix_ok && shared_seq_ok(p, own_L, P) && own_s < p.num_seqs ? own_L : INT32_MAX;
+    const long long mine = ahead;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, ahead, o);
+      if (lane >= o) ahead += y;
+    }
+    if (lane == 31) sums[warp] = ahead;
+    ahead -= mine;
+    long long more = 0;
+    for (int s = own_s + C::kThreads; s < p.num_seqs; s += C::kThreads) {
       const int L = __ldg(p.context_lens + s);
       if (prefix_ok && shared_seq_ok(p, L, P)) m = min(m, L);
-      u += own_units(L);
+      const int t = own_tiles(L);
+      more += ((long long)t << 22) + (t > 0);
     }
     m = __reduce_min_sync(0xffffffffu, m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (lane == 0 && m != INT32_MAX) {
-      atomicMin(misc + 2, m);
-      atomicAdd(reinterpret_cast<unsigned long long*>(misc + 6), (unsigned long long)u);
-    }
+    if (lane == 0 && m != INT32_MAX) atomicMin(misc + 2, m);
+    if (p.num_seqs > C::kThreads && more != 0)
+      atomicAdd(reinterpret_cast<unsigned long long*>(misc + 6), (unsigned long long)more);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
+  long long both = *reinterpret_cast<long long*>(misc + 6);
+#pragma unroll
+  for (int x = 0; x < C::kThreads / 32; ++x) {
+    const long long y = sums[x];
+    if (x < warp) ahead += y;
+    both += y;
+  }
   int vlo = 0, vhi = -1;  // the prefix's visible keys: from the shortest sequence's first on
   if (misc[2] != INT32_MAX) {
     int hi;
@@ -309,49 +334,56 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   const int uh = (R + 127) / 128;                           // ... of all row tiles of a head
   const int NT = (R + p.row_tile - 1) / p.row_tile;
   const long long Wp = (long long)p.num_kv_heads * uh * nt;
-  const long long W = Wp + *reinterpret_cast<long long*>(misc + 6);
+  // A call with a tile for every CTA at most: none gets two.
+  const int start = Wp + (both >> 22) * hp <= p.ctas ? 0 : kOwnStart;
+  auto own_units = [&](long long tiles_and_seqs) {
+    return hp * ((tiles_and_seqs >> 22) + start * (tiles_and_seqs & 0x3fffff));
+  };
+  const long long W = Wp + own_units(both);
   // a range holds the beginning of a tile at least: no CTA between two
   // segments of a group is without one
-  const int Ce = (int)min(W / u1 > 1 ? W / u1 : 1, (long long)p.ctas);
+  const int Ce = (int)min(max(u1 == 2 ? W >> 1 : W, 1LL), (long long)p.ctas);
   const int cta = blockIdx.x;
   long long a = 0, b = 0;
   if (cta < Ce) {
-    a = cta * W / Ce;
-    b = (cta + 1) * W / Ce;
+    a = div_pos(cta * W, Ce);
+    b = div_pos((cta + 1) * W, Ce);
   }
   if (cta == 0 && threadIdx.x == 0) p.meta[0] = nt;  // for the join
-  if (a > Wp) {  // the sequence in which this CTA's range begins (as b > a, the whole CTA is here)
-    long long run = Wp;
-    long long* sums = reinterpret_cast<long long*>(smem + C::kK);  // [warps], no copy is in flight yet
-    for (int s0 = 0; s0 < p.num_seqs && run <= a; s0 += C::kThreads) {
-      const int s = s0 + threadIdx.x;
-      const long long u = s < p.num_seqs ? own_units(__ldg(p.context_lens + s)) : 0;
-      long long x = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) sums[warp] = x;
-      __syncthreads();
-      long long before = run, total = 0;
-      for (int w = 0; w < C::kThreads / 32; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-      }
-      const long long at = before + x - u;
-      if (at <= a && a < at + u) {
-        misc[3] = s;
-        *reinterpret_cast<long long*>(misc + 4) = at;
-      }
-      run += total;
-      __syncthreads();
-    }
-    fence_proxy_async_smem();
-  } else if (threadIdx.x == 0) {
+  // The sequence in which this CTA's range begins, where it begins behind the
+  // prefix.
+  if (threadIdx.x == 0 && a <= Wp) {
     misc[3] = 0;
     *reinterpret_cast<long long*>(misc + 4) = Wp;
   }
+  if (a > Wp) {
+    const long long at = Wp + own_units(ahead), u = own_units(((long long)own_t << 22) + (own_t > 0));
+    if (at <= a && a < at + u) {
+      misc[3] = own_s;
+      *reinterpret_cast<long long*>(misc + 4) = at;
+    }
+    if (p.num_seqs > C::kThreads && warp == 0) {  // the further rounds, 32 sequences at a time
+      long long run = 0;
+      for (int x = 0; x < C::kThreads / 32; ++x) run += sums[x];
+      for (int s0 = C::kThreads; s0 < p.num_seqs && Wp + own_units(run) <= a; s0 += 32) {
+        const int s = s0 + lane, t = s < p.num_seqs ? own_tiles(__ldg(p.context_lens + s)) : 0;
+        const long long mine = ((long long)t << 22) + (t > 0);
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const long long first = Wp + own_units(run + x - mine);
+        if (first <= a && a < first + own_units(mine)) {
+          misc[3] = s;
+          *reinterpret_cast<long long*>(misc + 4) = first;
+        }
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+  }
+  fence_proxy_async_smem();  // the sums lie where copies will land
   __syncthreads();
 
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegs);
@@ -601,9 +633,10 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     segments([&](const Segment& g) {
       if (!ok) return;
       const int gn = __reduce_max_sync(0xffffffffu, g.n);
-      const bool dual = !kQuant && (__reduce_max_sync(0xffffffffu, g.flags) & kDual);
+      const int flags = __reduce_max_sync(0xffffffffu, g.flags);
+      const bool dual = !kQuant && (flags & kDual);
       const int Y = dual ? 2 * gn : gn;  // steps of the stream
-      const uint64_t q = dQ + (dual ? (uint64_t)(w * kTileBytes) >> 4 : 0);
+      const uint64_t q = dQ + ((dual ? w : (flags & kBuf) ? 1 : 0) * kTileBytes >> 4);
       ok = wait1(BAR_QFULL, seg);
       if (!ok) return;
       // S of step y (its buffer (c + y) & 1), products of K's high parts, then
@@ -636,7 +669,8 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       for (int y = 0; y < Y && ok; ++y) {
         const int half = dual ? y & 1 : w, buf = (c + y) & 1;
         ok = wait1(BAR_PFULL + w * 2 + buf, (c + y) >> 1) &&
-             ((dual && half == 1) || wait1(BAR_VFULL + vs, vp));
+             ((dual && half == 1) || wait1(BAR_VFULL + vs, vp)) &&
+             (y > 0 || seg == 0 || wait1(BAR_OEMPTY, seg - 1));
         if (!ok) break;
         tc_fence_after();
         const uint32_t pb = tm + w * 128 + buf * kStep;
@@ -675,11 +709,14 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   } else if (warp == C::kMmaWarp + 2) {
     // ===================== segments =========================================
     if (lane == 0) {
-      int count = 0;
+      int count = 0, buf = kBuf;
       auto publish = [&](const Segment& g) {
         const int st = count % kSegSlots;
         if (!seg_wait(BAR_GEMPTY + st, (count / kSegSlots) ^ 1)) return;
         segs[st] = g;
+        // Q of a single segment: the two buffers in turn (one buffer for int8).
+        buf = kQuant || (g.flags & kDual) ? 0 : buf ^ kBuf;
+        segs[st].flags |= buf;
         mbar_arrive(bar(BAR_GFULL + st));
         ++count;
       };
@@ -687,14 +724,14 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       while (x < b && x < Wp) {
         Segment g;
         const long long head = (long long)uh * nt, tile = (long long)u1 * nt;
-        g.kvh = (int)(x / head);
-        const int i = (int)((x - g.kvh * head) / tile);
+        g.kvh = (int)div_pos(x, head);
+        const int i = (int)div_pos(x - g.kvh * head, tile);
         const long long at = g.kvh * head + i * tile;
         g.row0 = i * p.row_tile;
         g.nrows = min(R - g.row0, p.row_tile);
-        const int u = g.nrows > 128 ? 2 : 1;
-        g.t0 = (int)((x - at + u - 1) / u);
-        const int te = (int)min((long long)nt, (b - at + u - 1) / u);
+        const int u = g.nrows > 128 ? 2 : 1, u_log = u - 1;
+        g.t0 = (int)((x - at + u - 1) >> u_log);
+        const int te = (int)min((long long)nt, (b - at + u - 1) >> u_log);
         g.n = te - g.t0;
         g.table = p.prefix_table;
         g.lo = vlo;
@@ -712,14 +749,14 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       for (int s = misc[3]; x < b && s < p.num_seqs; ++s) {
         Segment g;
         own_keys(__ldg(p.context_lens + s), g.lo, g.hi);
-        const int tiles = key_tiles(g.lo, g.hi), len = tiles + kOwnStart;
+        const int tiles = key_tiles(g.lo, g.hi), len = tiles + start;
         if (tiles == 0) continue;
         g.table = p.block_table + (long long)s * p.max_blocks_per_seq;
         g.base = g.lo / kChunk * kChunk;
         g.clo = P;
         g.chi = INT32_MAX;
-        for (int j = (int)((x - at) / len); j < hp && x < b; ++j) {
-          const long long st = at + (long long)j * len + kOwnStart;  // unit of the first tile
+        for (int j = (int)div_pos(x - at, len); j < hp && x < b; ++j) {
+          const long long st = at + (long long)j * len + start;  // unit of the first tile
           const int part = j % p.parts;
           g.kvh = j / p.parts;
           g.row0 = s * p.rows_seq + part * p.rows_part;
@@ -748,31 +785,44 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale negates Q
     int T0 = 0, c0 = 0, seg = 0;  // tiles, steps and segments before
     bool ok = true;
-    segments([&](const Segment& g) {
+    // Stages this warpgroup's share of a segment's Q rows.
+    auto stage_q = [&](const Segment& g) {
+      const bool dual = !kQuant && (g.flags & kDual);
+      const int local = (dual ? w * 128 : 0) + r, row = g.row0 + local;
+      const bool in = local < g.nrows;
+      const __half* src = p.q + ((long long)(in ? row / p.group : 0) * p.num_q_heads + g.kvh * p.group +
+                                 (in ? row % p.group : 0)) * kHeadDim;
+      const uint32_t dst = sQ + ((dual ? w : (g.flags & kBuf) ? 1 : 0) * kTileBytes) +
+                           (r / 8) * kGroupBytes + (r % 8) * 128;
+      const int c_lo = dual ? 0 : w * 8, c_hi = dual ? 16 : w * 8 + 8;
+#pragma unroll 1
+      for (int c0 = c_lo; c0 < c_hi; c0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[c] = make_uint4(0, 0, 0, 0);
+          if (in) v[c] = __ldg(reinterpret_cast<const uint4*>(src) + c0 + c);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[c].x ^= flip; v[c].y ^= flip; v[c].z ^= flip; v[c].w ^= flip;
+          sts_v4(dst + (c0 / 8) * kAtomBytes + ((c ^ (r % 8)) * 16), in ? v[c] : make_uint4(0, 0, 0, 0));
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_QFULL));
+    };
+    bool got = __all_sync(0xffffffffu, seg_wait(BAR_GFULL, 0));
+    if (got && segs[0].n != 0) stage_q(segs[0]);
+    else got = false;
+    while (got) {
+      const Segment& g = segs[seg % kSegSlots];
       const bool dual = !kQuant && (g.flags & kDual);
       const int local = (dual ? w * 128 : 0) + r, row = g.row0 + local;
       const bool mine = local < g.nrows;
       const int tok = row / p.group;  // of all sequences' new tokens
-      // ---- Q: this warpgroup's share of the rows' columns ---------------------
-      {
-        const __half* src = p.q + ((long long)(mine ? tok : 0) * p.num_q_heads + g.kvh * p.group +
-                                   (mine ? row % p.group : 0)) * kHeadDim;
-        const uint32_t dst = sQ + (dual ? w * kTileBytes : 0) + (r / 8) * kGroupBytes + (r % 8) * 128;
-        const int nc = dual ? 16 : 8, c_lo = dual ? 0 : w * 8, c_hi = c_lo + nc;
-#pragma unroll 8
-        for (int c = c_lo; c < c_hi; ++c) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (mine) {
-            v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-          }
-          sts_v4(dst + (c / 8) * kAtomBytes + (((c % 8) ^ (r % 8)) * 16), v);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_QFULL));
-      }
       // ---- this row's keys ----------------------------------------------------
       int lo = 0, hi = -1;
       if (mine) {
@@ -911,10 +961,12 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           if (__any_sync(0xffffffffu, need)) {
             // Rows over the limit and rows at their first keys: the reference
             // becomes the step's maximum; the scores are read again.
-            tmem_ld32(tS, va);
-            tmem_ld32(tS + 32, vb);
-            tmem_ld_wait(va);
-            tmem_ld_wait(vb);
+            if (y > 0) {
+              tmem_ld32(tS, va);
+              tmem_ld32(tS + 32, vb);
+              tmem_ld_wait(va);
+              tmem_ld_wait(vb);
+            }
             scaled(va, 0);
             scaled(vb, 1);
             float mx = -INFINITY;
@@ -984,6 +1036,11 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       }
       if (!ok) tmem_ld_wait();
       // ---- the segment's partial ------------------------------------------------
+      // The next segment's Q goes into the other buffer, where there is one.
+      const Segment& gn = segs[(seg + 1) % kSegSlots];
+      bool more = __all_sync(0xffffffffu, seg_wait(BAR_GFULL + (seg + 1) % kSegSlots, (seg + 1) / kSegSlots));
+      const bool q_ahead = !kQuant && more && gn.n != 0 && !dual && !(gn.flags & kDual);
+      if (q_ahead) stage_q(gn);
       ok = __all_sync(0xffffffffu, ok && wait(BAR_SEG, seg));
       bool row_bad = false;
       if (*reinterpret_cast<volatile int*>(misc + 9) != 0) {  // rows that see an out-of-range block
@@ -998,12 +1055,13 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
         if (g.flags & kLast) p.meta[3 + 2 * g.group] = cta;
       }
       // Every warpgroup's m and l of its rows, through Q's buffer (it has been read).
-      float2* stat = reinterpret_cast<float2*>(smem + C::kQ);  // [2][128]
+      const uint32_t q_off = !dual && (g.flags & kBuf) ? kTileBytes : 0;
+      float2* stat = reinterpret_cast<float2*>(smem + C::kQ + q_off);  // [2][128]
       stat[w * 128 + r] = make_float2(row_bad ? __uint_as_float(kInvalidLse) : m, l);
       ok = named_bar_and(1, kSoftThreads, ok);
       const float2 s0 = stat[(dual ? w : 0) * 128 + r];
       const float2 s1 = dual ? make_float2(-INFINITY, 0.f) : stat[128 + r];
-      named_bar_sync(2, kSoftThreads);
+      more = named_bar_and(2, kSoftThreads, more);  // (the same for all)
       // single: the two streams' sums; f0, f1: the accumulators' factors
       const bool bad = !ok || isnan(s0.x + s0.y) || isnan(s1.x + s1.y);
       const float mm = fmaxf(s0.x, s1.x);
@@ -1019,7 +1077,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
         const float inv = ll > 0.f ? 1.f / ll : 0.f;
         const float f0 = w0 * inv, f1 = w1 * inv;
         const int nx = dual ? 4 : 2, x0 = dual ? 0 : w * 2;  // this warpgroup's chunks of 32 columns
-        const uint32_t stage = sQ + warp * 4096;
+        const uint32_t stage = sQ + q_off + warp * 4096;
         float* out = p.part_out + (g.out_row + local - lane) * kHeadDim;     // the warp's first row
 #pragma unroll 1
         for (int c = x0; c < x0 + nx; ++c) {
@@ -1055,11 +1113,17 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           __syncwarp();
         }
       }
-      named_bar_sync(3, kSoftThreads);  // Q may be staged again
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_OEMPTY));
       T0 += g.n;
       c0 += Y;
+      if (lane == 0) mbar_arrive(bar(BAR_GEMPTY + seg % kSegSlots));
       ++seg;
-    });
+      named_bar_sync(3, kSoftThreads);  // this segment's buffer may be staged again
+      got = more && gn.n != 0;
+      if (got && !q_ahead) stage_q(gn);
+    }
   }
   tc_fence_before();
   __syncthreads();
