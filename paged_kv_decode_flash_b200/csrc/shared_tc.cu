@@ -40,7 +40,7 @@
 //
 // Roles: warps 0-7 the softmax, which also stages Q and writes the partials.
 // Then, fp16: a producer (TMA boxes of 16 keys through the block table);
-// int8: four converters (raw bytes through registers, one tile ahead).  Then
+// int8: eight converters (raw bytes through registers, one tile ahead).  Then
 // an MMA issuer for each stream (one for both was the bottleneck: with the
 // waits, a step's sixteen products take a warp 1750 cycles to issue and the
 // tensor cores 780), and a warp that cuts the CTA's range into segments.
@@ -75,6 +75,7 @@ constexpr uint32_t kChunkBytes = kChunk * 256;
 // fp16's range cuts off.
 constexpr float kShift = 2.f;
 constexpr float kSumLimit = 32768.f;
+constexpr float kLazy = 13.f;  // int8: a row whose maximum passes its reference by this moves it
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kInvalidLse = 0x7fc00000u;  // NaN: a partial that must not be used
 constexpr int kStep = 64;       // keys of a step of a stream
@@ -105,9 +106,9 @@ struct Cfg {
   static constexpr bool kQuant = KV != kKvFp16;
   static constexpr bool kQ8 = KV == kKvQ8_0, kRow = KV == kKvInt8Row;
   static constexpr int kProdWarp = 8;                      // fp16: producer; int8: converters
-  static constexpr int kMmaWarp = kProdWarp + (kQuant ? 4 : 1);  // [2], then the segments' warp
+  static constexpr int kMmaWarp = kProdWarp + (kQuant ? 8 : 1);  // [2], then the segments' warp
   static constexpr int kReaders = kMmaWarp + 2;            // warps that follow the segments
-  static constexpr int kThreads = kQuant ? 480 : 384;
+  static constexpr int kThreads = kQuant ? 640 : 384;
   static constexpr uint32_t kSlot = (kQ8 ? 2 : 1) * kTileBytes;  // q8_0: the high tile, the residual
   static constexpr int KS = kQ8 ? 1 : kRow ? 2 : 3;
   static constexpr int VS = kRow ? 3 : 2;
@@ -407,77 +408,104 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       // ===================== int8 converters ================================
       // A warp takes 32 keys of every tile, eight lanes a key: coalesced loads
       // into registers one tile ahead, then the operand layout.
+      const bool isk = warp < C::kProdWarp + 4;  // four warps for K, four for V
       const int cw = warp % 4, kq = lane / 8, cl = lane % 8;
+      const int NS = isk ? C::KS : C::VS;
+      const uint32_t ring = isk ? sK : sV;
+      const int full = isk ? BAR_KFULL : BAR_VFULL, empty = isk ? BAR_KEMPTY : BAR_VEMPTY;
+      const uint8_t* cache = static_cast<const uint8_t*>(isk ? p.k : p.v);
       const long long tile_bytes = quant_tile_bytes(KV, p.block_size);
-      struct Raw {  // 32 keys of K or V
-        uint4 q[8];
-        uint16_t d8[kQ8 ? 8 : 1];  // q8_0: the scale of this lane's 16 values
-        float d1;                  // int8 rows: the scale of key `lane`
-      };
-      int T = 0;
+      float* scales = reinterpret_cast<float*>(smem + C::kScales);  // K [8][128], V, max [8][4]
+      int T = 0, st = 0, ph = 0;
       bool ok = true;
       segments([&](const Segment& g) {
         const int base = g.base, t0 = g.t0, te = g.t0 + g.n, vlo = g.lo, vhi = g.hi;
         const int32_t* table = g.table;
+        uint4 q[8];                    // 32 keys' values
+        uint16_t d8[kQ8 ? 8 : 1];      // q8_0: the scales of this lane's 16 values
+        float d1 = 0.f;                // int8 rows: the scale of key `lane`
         // The block of this warp's two chunks of tile t (lanes 0, 1).
         auto lookup = [&](int t) -> int {
           const int key0 = base + t * kTileKeys + (2 * cw + lane) * kChunk;
-          return lane < 2 && t < te && key0 <= vhi ? __ldg(table + key0 / p.block_size) : 0;
+          int phys = lane < 2 && t < te && key0 <= vhi ? __ldg(table + key0 / p.block_size) : 0;
+          if (phys < 0 || phys >= p.num_blocks) {
+            misc[9] = 1;
+            atomicOr(p.flags, kFlagBadBlock);
+            phys = 0;  // a stand-in: the rows that see it are marked
+          }
+          return phys;
         };
-        auto fetch = [&](const void* cache, int t, int phys, Raw& x) {
-          x.d1 = 0.f;
+        auto fetch = [&](int t, int phys) {
+          d1 = 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int key0 = base + t * kTileKeys + (2 * cw + h) * kChunk;
-            const long long ph = __shfl_sync(0xffffffffu, phys, h);
+            const long long b = __shfl_sync(0xffffffffu, phys, h);
             const bool on = t < te && key0 <= vhi;
-            const uint8_t* tile =
-                static_cast<const uint8_t*>(cache) + (ph * p.num_kv_heads + g.kvh) * tile_bytes;
+            const uint8_t* tile = cache + (b * p.num_kv_heads + g.kvh) * tile_bytes;
             const int slot = key0 % p.block_size;
+            const uint8_t* at = tile + (slot + kq) * kHeadDim + cl * 16;
+            const uint8_t* sc = tile + p.block_size * kHeadDim + (slot + kq) * 8 + cl / 2 * 2;
 #pragma unroll
             for (int i = 4 * h; i < 4 * h + 4; ++i) {
-              const int k = slot + (4 * i) % kChunk + kq;
-              x.q[i] = make_uint4(0, 0, 0, 0);
-              if constexpr (kQ8) x.d8[i] = 0;
+              q[i] = make_uint4(0, 0, 0, 0);
+              if constexpr (kQ8) d8[i] = 0;
               if (on) {
-                x.q[i] = __ldg(reinterpret_cast<const uint4*>(tile + k * kHeadDim) + cl);
-                if constexpr (kQ8)
-                  x.d8[i] = __ldg(reinterpret_cast<const unsigned short*>(
-                                      tile + p.block_size * kHeadDim + k * 8) + cl / 2);
+                q[i] = __ldg(reinterpret_cast<const uint4*>(at + i % 4 * 4 * kHeadDim));
+                if constexpr (kQ8) d8[i] = __ldg(reinterpret_cast<const unsigned short*>(sc + i % 4 * 32));
               }
             }
             if constexpr (kRow) {
               if (on && lane / kChunk == h)
-                x.d1 = __ldg(reinterpret_cast<const float*>(tile + p.block_size * kHeadDim) + slot +
-                             lane % kChunk);
+                d1 = __ldg(reinterpret_cast<const float*>(tile + p.block_size * kHeadDim) + slot +
+                           lane % kChunk);
             }
           }
         };
-        // Writes the operand tile at `slot`; keys outside [klo, vhi] get scale 0.
-        auto convert = [&](const Raw& x, uint32_t slot, int kw, int klo) {
+        fetch(t0, lookup(t0));
+        int phys = lookup(t0 + 1);
+        const bool sw = cl >= 4;
+        const uint32_t row0 = 4 * cw * kGroupBytes + kq * 128 + (cl / 4) * kAtomBytes;
+        for (int t = t0; t < te && ok; ++t, ++T) {
+          const int kw = base + t * kTileKeys + 32 * cw, ss = T % kScaleSlots;
+          ok = __all_sync(0xffffffffu, wait(empty + st, ph ^ 1));
+          if (!ok) break;
+          if constexpr (kRow) {
+            if (isk) {
+              scales[ss * 128 + 32 * cw + lane] = d1 * cs;
+            } else {  // scales of hidden keys may be anything
+              const float d = kw + lane >= vlo && kw + lane <= vhi ? d1 : 0.f;
+              float mx = fabsf(d);
+              scales[(kScaleSlots + ss) * 128 + 32 * cw + lane] = d;
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              if (lane == 0) scales[2 * kScaleSlots * 128 + ss * 4 + cw] = mx;
+            }
+          }
+          const bool inside = isk || (kw >= vlo && kw + 31 <= vhi);
+          const uint32_t dst = ring + st * C::kSlot + row0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int r = 32 * cw + 4 * i + kq;
-            const uint32_t dst = slot + (r / 8) * kGroupBytes + (r % 8) * 128 + (cl / 4) * kAtomBytes;
+            // Row 32 cw + 4 i + kq.  Lanes 4-7 of a key write their second half
+            // first: the eight lanes of a store then cover all banks.
+            const int r8 = 4 * (i & 1) + kq;
+            const uint32_t at = dst + (i / 2) * kGroupBytes + (i & 1) * 512;
+            const uint32_t a0 = at + (((2 * cl + sw) % 8) ^ r8) * 16, a1 = at + (((2 * cl + 1 - sw) % 8) ^ r8) * 16;
+            const uint32_t wd[4] = {sw ? q[i].z : q[i].x, sw ? q[i].w : q[i].y, sw ? q[i].x : q[i].z,
+                                    sw ? q[i].y : q[i].w};
             __half2 y[8];
-            const uint32_t wd[4] = {x.q[i].x, x.q[i].y, x.q[i].z, x.q[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) q8_to_half4(wd[e], y[2 * e], y[2 * e + 1]);
-            // Lanes 4-7 of a key write their second half first: the eight
-            // lanes of a store then cover all banks.
-            const int sw = cl >= 4;
-            const uint32_t a0 = dst + (((2 * cl + sw) % 8) ^ (r % 8)) * 16;
-            const uint32_t a1 = dst + (((2 * cl + 1 - sw) % 8) ^ (r % 8)) * 16;
             auto put = [&](const __half2 (&h)[8], uint32_t off) {
-              const uint4 u0 = make_uint4(h2_bits(h[0]), h2_bits(h[1]), h2_bits(h[2]), h2_bits(h[3]));
-              const uint4 u1 = make_uint4(h2_bits(h[4]), h2_bits(h[5]), h2_bits(h[6]), h2_bits(h[7]));
-              sts_v4(a0 + off, sw ? u1 : u0);
-              sts_v4(a1 + off, sw ? u0 : u1);
+              sts_v4(a0 + off, make_uint4(h2_bits(h[0]), h2_bits(h[1]), h2_bits(h[2]), h2_bits(h[3])));
+              sts_v4(a1 + off, make_uint4(h2_bits(h[4]), h2_bits(h[5]), h2_bits(h[6]), h2_bits(h[7])));
             };
             if constexpr (kQ8) {
-              __half d = __ushort_as_half(x.d8[i]);
-              const int key = kw + 4 * i + kq;
-              if (key < klo || key > vhi) d = __ushort_as_half(0);
+              __half d = __ushort_as_half(d8[i]);
+              if (!inside) {  // hidden keys' scales may be anything
+                const int key = kw + 4 * i + kq;
+                if (key < vlo || key > vhi) d = __ushort_as_half(0);
+              }
               const __half2 d2 = __halves2half2(d, d);
               __half2 hi8[8];
 #pragma unroll
@@ -491,54 +519,15 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               put(y, 0);
             }
           }
-        };
-        float* scales = reinterpret_cast<float*>(smem + C::kScales);  // K [8][128], V, max [8][4]
-        Raw k, v;
-        int phys = 0;
-        uint32_t bad = 0, bad_next = 0;  // out-of-range blocks of this warp's chunks
-        auto next = [&](int t) {         // tile t's blocks
-          phys = lookup(t);
-          const bool b = phys < 0 || phys >= p.num_blocks;
-          bad_next = __ballot_sync(0xffffffffu, b);
-          if (b) phys = 0;  // a stand-in: the rows that see it are marked
-        };
-        next(t0);
-        bad = bad_next;
-        fetch(p.k, t0, phys, k);
-        fetch(p.v, t0, phys, v);
-        next(t0 + 1);
-        for (int t = t0; t < te; ++t, ++T) {
-          const int kw = base + t * kTileKeys + 32 * cw;
-          const int sk = T % C::KS, sv = T % C::VS, ss = T % kScaleSlots;
-          ok = ok && __all_sync(0xffffffffu, wait(BAR_KEMPTY + sk, (T / C::KS) ^ 1));
-          if (!ok) break;
-          if (bad && lane == 0) {
-            misc[9] = 1;
-            atomicOr(p.flags, kFlagBadBlock);
-          }
-          if constexpr (kRow) scales[ss * 128 + 32 * cw + lane] = k.d1 * cs;
-          convert(k, sK + sk * C::kSlot, kw, 0);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_KFULL + sk));
-          fetch(p.k, t + 1, phys, k);
-          ok = __all_sync(0xffffffffu, wait(BAR_VEMPTY + sv, (T / C::VS) ^ 1));
-          if (!ok) break;
-          if constexpr (kRow) {  // scales of hidden keys may be anything
-            const float d = kw + lane >= vlo && kw + lane <= vhi ? v.d1 : 0.f;
-            float mx = fabsf(d);
-            scales[(kScaleSlots + ss) * 128 + 32 * cw + lane] = d;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) scales[2 * kScaleSlots * 128 + ss * 4 + cw] = mx;
+          if (lane == 0) mbar_arrive(bar(full + st));
+          fetch(t + 1, phys);
+          phys = lookup(t + 2);
+          if (++st == NS) {
+            st = 0;
+            ph ^= 1;
           }
-          convert(v, sV + sv * C::kSlot, kw, vlo);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_VFULL + sv));
-          fetch(p.v, t + 1, phys, v);
-          bad = bad_next;
-          next(t + 2);
         }
       });
     }
@@ -780,6 +769,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     // ===================== softmax warpgroups ===============================
     const int w = warp / 4, r = threadIdx.x % 128;
     constexpr int kSoftThreads = 256;
+    constexpr bool kHold = !kQuant;  // a step's scores stay in registers
     const uint32_t lane_off = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t tO = tmem + lane_off + 256;
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale negates Q
@@ -842,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       const int whi = __reduce_min_sync(0xffffffffu, mine ? min(hi, g.hi) : g.hi);
       const int glo = g.lo, ghi = g.hi, key0 = g.base + g.t0 * kTileKeys;
       // S of step y: awaited and (its first or second 32 columns) loaded.
-      float va[32], vb[32];
+      float va[32], vb[kHold ? 32 : 1];
       auto s_wait = [&](int y) -> bool {
         const int c = c0 + y;
         const bool got = __all_sync(0xffffffffu, wait(BAR_SFULL + w * 2 + (c & 1), c >> 1));
@@ -867,7 +857,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           ok = s_wait(y);
           if (!ok) break;
           s_load(y, 0, va);
-          s_load(y, 1, vb);
+          if constexpr (kHold) s_load(y, 1, vb);
         }
         early = false;
         // Keys that no row sees must not reach PV: their V rows become 0 (in a
@@ -938,41 +928,9 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               sum = add2(sum, make_float2(v[e], v[e + 1]));
             }
           };
-          auto all_weights = [&]() -> float {
-            scaled(va, 0);
-            scaled(vb, 1);
-            sum = make_float2(0.f, 0.f);
-            weights(va);
-            weights(vb);
-            return sum.x + sum.y;
-          };
-          tmem_ld_wait(va);
-          tmem_ld_wait(vb);
-          // The weights against the reference so far; a row whose sum (times
-          // the largest |V scale|) stays below the limit keeps it, without its
-          // maximum ever being taken.
-          float total = 0.f;
-          bool need = mine;
-          if (y > 0) {
-            total = all_weights();
-            const float most = kRow ? total * fast_exp2(vtop) : total;
-            need = mine && (m == -INFINITY || !(most <= kSumLimit));
-          }
-          if (__any_sync(0xffffffffu, need)) {
-            // Rows over the limit and rows at their first keys: the reference
-            // becomes the step's maximum; the scores are read again.
-            if (y > 0) {
-              tmem_ld32(tS, va);
-              tmem_ld32(tS + 32, vb);
-              tmem_ld_wait(va);
-              tmem_ld_wait(vb);
-            }
-            scaled(va, 0);
-            scaled(vb, 1);
-            float mx = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = max3(mx, va[e], vb[e]);
-            const float top = (kRow ? mx : mx * cs) + vtop;
+          // Moves the reference of the rows that `need` it to `top`, and what the
+          // stream has accumulated for them.
+          auto move = [&](bool need, float top) -> bool {
             const float mn = need && top != -INFINITY ? top : m;
             const bool moved = mn != m;
             const float f = moved ? fast_exp2(m - mn) : 1.f;
@@ -983,7 +941,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               // rescale what this stream has accumulated, once the last step's
               // PV is done (S of the next step is committed behind it)
               ok = y + 1 < Y ? s_wait(y + 1) : __all_sync(0xffffffffu, wait(BAR_OFULL + w, seg)) != 0;
-              if (!ok) break;
+              if (!ok) return false;
               tc_fence_after();
 #pragma unroll 1
               for (int x = 0; x < 8; ++x) {
@@ -996,12 +954,14 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               }
               tmem_st_wait();
             }
-            sum = make_float2(0.f, 0.f);
-            weights(va);
-            weights(vb);
-            total = sum.x + sum.y;
-          }
-          l += total;
+            return true;
+          };
+          auto top_of = [&](const float (&v)[32]) -> float {
+            float mx = v[0];
+#pragma unroll
+            for (int e = 1; e < 31; e += 2) mx = max3(mx, v[e], v[e + 1]);
+            return fmaxf(mx, v[31]);
+          };
           // Weights of 32 keys over their scores: 16 columns of high parts, 16
           // of residuals (exact: w - fp16(w) fits fp32).
           auto store = [&](const float (&v)[32], int c) {
@@ -1021,13 +981,80 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               tmem_st8(tS + c * 32 + 16 + y * 8, pl);
             }
           };
-          // Where the next step's scores are there, they are loaded behind this
-          // one's weights.
-          early = y + 1 < Y && s_there(y + 1);
-          store(va, 0);
-          if (early) s_load(y + 1, 0, va);
-          store(vb, 1);
-          if (early) s_load(y + 1, 1, vb);
+          if constexpr (!kHold) {
+            // Two passes over S in TMEM, 32 columns at a time: the converters
+            // leave no registers for a step's 64 scores.
+            tmem_ld_wait(va);
+            scaled(va, 0);
+            float mx = top_of(va);
+            tmem_ld32(tS + 32, va);
+            tmem_ld_wait(va);
+            scaled(va, 1);
+            mx = fmaxf(mx, top_of(va));
+            const float top = (kRow ? mx : mx * cs) + vtop;
+            const bool raise = mine && top > m + kLazy;
+            if (__any_sync(0xffffffffu, raise) && !move(raise, top)) break;
+            sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              tmem_ld32(tS + x * 32, va);
+              tmem_ld_wait(va);
+              scaled(va, x);
+              weights(va);
+              store(va, x);
+            }
+            l += sum.x + sum.y;
+          } else {
+            auto all_weights = [&]() -> float {
+              scaled(va, 0);
+              scaled(vb, 1);
+              sum = make_float2(0.f, 0.f);
+              weights(va);
+              weights(vb);
+              return sum.x + sum.y;
+            };
+            tmem_ld_wait(va);
+            tmem_ld_wait(vb);
+            // The weights against the reference so far; a row whose sum (times
+            // the largest |V scale|) stays below the limit keeps it, without its
+            // maximum ever being taken.
+            float total = 0.f;
+            bool need = mine;
+            if (y > 0) {
+              total = all_weights();
+              const float most = kRow ? total * fast_exp2(vtop) : total;
+              need = mine && (m == -INFINITY || !(most <= kSumLimit));
+            }
+            if (__any_sync(0xffffffffu, need)) {
+              // Rows over the limit and rows at their first keys: the reference
+              // becomes the step's maximum; the scores are read again.
+              if (y > 0) {
+                tmem_ld32(tS, va);
+                tmem_ld32(tS + 32, vb);
+                tmem_ld_wait(va);
+                tmem_ld_wait(vb);
+              }
+              scaled(va, 0);
+              scaled(vb, 1);
+              float mx = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx = max3(mx, va[e], vb[e]);
+              const float top = (kRow ? mx : mx * cs) + vtop;
+              if (!move(need, top)) break;
+              sum = make_float2(0.f, 0.f);
+              weights(va);
+              weights(vb);
+              total = sum.x + sum.y;
+            }
+            l += total;
+            // Where the next step's scores are there, they are loaded behind this
+            // one's weights.
+            early = y + 1 < Y && s_there(y + 1);
+            store(va, 0);
+            if (early) s_load(y + 1, 0, va);
+            store(vb, 1);
+            if (early) s_load(y + 1, 1, vb);
+          }
           tmem_st_wait();
         }
         tc_fence_before();
