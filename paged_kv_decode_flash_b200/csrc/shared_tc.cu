@@ -79,7 +79,9 @@ constexpr float kLazy = 13.f;  // int8: a row whose maximum passes its reference
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kInvalidLse = 0x7fc00000u;  // NaN: a partial that must not be used
 constexpr int kStep = 64;       // keys of a step of a stream
-constexpr int kOwnStart = 3;    // what the start of an own-keys segment costs, in units
+// What the start of an own-keys segment costs (5 us), in units: 1.4 us each where
+// two of them are a dual segment's tile, else 2 to 2.5 us.
+constexpr int kOwnStart = 4;
 constexpr int kScaleSlots = 8;  // tiles whose row scales are kept: more than are in flight
 
 constexpr int kSegSlots = 4;
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   const int NT = (R + p.row_tile - 1) / p.row_tile;
   const long long Wp = (long long)p.num_kv_heads * uh * nt;
   // A call with a tile for every CTA at most: none gets two.
-  const int start = Wp + (both >> 22) * hp <= p.ctas ? 0 : kOwnStart;
+  const int start = Wp + (both >> 22) * hp <= p.ctas ? 0 : u1 == 2 ? kOwnStart : kOwnStart / 2;
   auto own_units = [&](long long tiles_and_seqs) {
     return hp * ((tiles_and_seqs >> 22) + start * (tiles_and_seqs & 0x3fffff));
   };
@@ -657,9 +659,9 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       if (ok && Y > 1) scores(1);
       for (int y = 0; y < Y && ok; ++y) {
         const int half = dual ? y & 1 : w, buf = (c + y) & 1;
-        ok = wait1(BAR_PFULL + w * 2 + buf, (c + y) >> 1) &&
-             ((dual && half == 1) || wait1(BAR_VFULL + vs, vp)) &&
-             (y > 0 || seg == 0 || wait1(BAR_OEMPTY, seg - 1));
+        ok = ((dual && half == 1) || wait1(BAR_VFULL + vs, vp)) &&  // (there before P as a rule)
+             (y > 0 || seg == 0 || wait1(BAR_OEMPTY, seg - 1)) &&
+             wait1(BAR_PFULL + w * 2 + buf, (c + y) >> 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t pb = tm + w * 128 + buf * kStep;
@@ -672,15 +674,17 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
                         vd + ((k * 2 * kGroupBytes + (part == 2) * kTileBytes) >> 4), id_pv,
                         y > 0 || i > 0);
         }
+        const int slot = vs;
         if (!dual || half == 1) {
-          tc_commit(lead, bar(BAR_VEMPTY + vs));
+          if (kQuant) tc_commit(lead, bar(BAR_VEMPTY + slot));  // (K may have to be waited for)
           if (++vs == C::VS) {
             vs = 0;
             vp ^= 1;
           }
         }
-        if (y == Y - 2) tc_commit(lead, bar(BAR_OFULL + w));
         if (y + 2 < Y) scores(y + 2);
+        if (!kQuant && (!dual || half == 1)) tc_commit(lead, bar(BAR_VEMPTY + slot));
+        if (y == Y - 2) tc_commit(lead, bar(BAR_OFULL + w));
       }
       if (ok) {
         if (Y == 1) tc_commit(lead, bar(BAR_OFULL + w));
@@ -839,27 +843,17 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
         tc_fence_after();
         return got;
       };
-      auto s_there = [&](int y) -> bool {
-        const int c = c0 + y;
-        const bool got = __all_sync(0xffffffffu, mbar_test_wait(bar(BAR_SFULL + w * 2 + (c & 1)), (c >> 1) & 1));
-        if (got) tc_fence_after();
-        return got;
-      };
       auto s_load = [&](int y, int x, float (&v)[32]) {
         if (warp_rows) tmem_ld32(tmem + lane_off + w * 128 + ((c0 + y) & 1) * kStep + x * 32, v);
       };
-      bool early = false;  // this step's scores are being loaded already
       for (int y = 0; y < Y && ok; ++y) {
         const int T = T0 + (dual ? y >> 1 : y), half = dual ? y & 1 : w, c = c0 + y;
         const int kb = key0 + (T - T0) * kTileKeys + half * kStep;  // the step's first key
         const uint32_t tS = tmem + lane_off + w * 128 + (c & 1) * kStep;
-        if (!early) {
-          ok = s_wait(y);
-          if (!ok) break;
-          s_load(y, 0, va);
-          if constexpr (kHold) s_load(y, 1, vb);
-        }
-        early = false;
+        ok = s_wait(y);
+        if (!ok) break;
+        s_load(y, 0, va);
+        if constexpr (kHold) s_load(y, 1, vb);
         // Keys that no row sees must not reach PV: their V rows become 0 (in a
         // dual segment by both streams, each before its own PV; the converters
         // see to that themselves).
@@ -917,15 +911,16 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             mask(v, c);
           };
           // Scores to weights, in place; their sum.
-          float2 sum;
+          float2 sum, sum2;
           auto weights = [&](float (&v)[32]) {
-            const float k = kRow ? 1.f : cs;
+            const float k = kRow ? 1.f : cs;  // (int8 rows: scaled already)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 z = fma2(make_float2(v[e], v[e + 1]), make_float2(k, k), make_float2(bias, bias));
               v[e] = fast_exp2(z.x);
               v[e + 1] = fast_exp2(z.y);
-              sum = add2(sum, make_float2(v[e], v[e + 1]));
+              float2& to = e & 2 ? sum2 : sum;
+              to = add2(to, make_float2(v[e], v[e + 1]));
             }
           };
           // Moves the reference of the rows that `need` it to `top`, and what the
@@ -964,22 +959,21 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           };
           // Weights of 32 keys over their scores: 16 columns of high parts, 16
           // of residuals (exact: w - fp16(w) fits fp32).
-          auto store = [&](const float (&v)[32], int c) {
+          constexpr int kPack = kHold ? 16 : 8;  // words of each at a time
+          uint32_t ph[kPack], pl[kPack];
+          auto pack = [&](const float (&v)[32], int c, int z) {  // from key 2 z of the chunk on
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t ph[8], pl[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int e = 16 * y + 2 * i;
-                float2 x = make_float2(v[e], v[e + 1]);
-                if constexpr (kRow) x = mul2(x, reinterpret_cast<const float2*>(vs)[c * 16 + e / 2]);
-                ph[i] = h2_bits(__floats2half2_rn(x.x, x.y));
-                const float2 lo2 = residual(x, ph[i]);
-                pl[i] = h2_bits(__floats2half2_rn(lo2.x, lo2.y));
-              }
-              tmem_st8(tS + c * 32 + y * 8, ph);
-              tmem_st8(tS + c * 32 + 16 + y * 8, pl);
+            for (int i = 0; i < kPack; ++i) {
+              float2 x = make_float2(v[2 * (z + i)], v[2 * (z + i) + 1]);
+              if constexpr (kRow) x = mul2(x, reinterpret_cast<const float2*>(vs)[c * 16 + z + i]);
+              ph[i] = h2_bits(__floats2half2_rn(x.x, x.y));
+              const float2 lo2 = residual(x, ph[i]);
+              pl[i] = h2_bits(__floats2half2_rn(lo2.x, lo2.y));
             }
+          };
+          auto put = [&](int c, int z) {
+            tmem_st(tS + c * 32 + z, ph);
+            tmem_st(tS + c * 32 + 16 + z, pl);
           };
           if constexpr (!kHold) {
             // Two passes over S in TMEM, 32 columns at a time: the converters
@@ -994,24 +988,28 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             const float top = (kRow ? mx : mx * cs) + vtop;
             const bool raise = mine && top > m + kLazy;
             if (__any_sync(0xffffffffu, raise) && !move(raise, top)) break;
-            sum = make_float2(0.f, 0.f);
+            sum = sum2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               tmem_ld32(tS + x * 32, va);
               tmem_ld_wait(va);
               scaled(va, x);
               weights(va);
-              store(va, x);
+#pragma unroll
+              for (int z = 0; z < 16; z += kPack) {
+                pack(va, x, z);
+                put(x, z);
+              }
             }
-            l += sum.x + sum.y;
+            l += (sum.x + sum.y) + (sum2.x + sum2.y);
           } else {
             auto all_weights = [&]() -> float {
               scaled(va, 0);
               scaled(vb, 1);
-              sum = make_float2(0.f, 0.f);
+              sum = sum2 = make_float2(0.f, 0.f);
               weights(va);
               weights(vb);
-              return sum.x + sum.y;
+              return (sum.x + sum.y) + (sum2.x + sum2.y);
             };
             tmem_ld_wait(va);
             tmem_ld_wait(vb);
@@ -1024,6 +1022,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               total = all_weights();
               const float most = kRow ? total * fast_exp2(vtop) : total;
               need = mine && (m == -INFINITY || !(most <= kSumLimit));
+              pack(va, 0, 0);  // (in the shadow of the vote)
             }
             if (__any_sync(0xffffffffu, need)) {
               // Rows over the limit and rows at their first keys: the reference
@@ -1041,19 +1040,16 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               for (int e = 0; e < 32; ++e) mx = max3(mx, va[e], vb[e]);
               const float top = (kRow ? mx : mx * cs) + vtop;
               if (!move(need, top)) break;
-              sum = make_float2(0.f, 0.f);
+              sum = sum2 = make_float2(0.f, 0.f);
               weights(va);
               weights(vb);
-              total = sum.x + sum.y;
+              total = (sum.x + sum.y) + (sum2.x + sum2.y);
+              pack(va, 0, 0);
             }
             l += total;
-            // Where the next step's scores are there, they are loaded behind this
-            // one's weights.
-            early = y + 1 < Y && s_there(y + 1);
-            store(va, 0);
-            if (early) s_load(y + 1, 0, va);
-            store(vb, 1);
-            if (early) s_load(y + 1, 1, vb);
+            put(0, 0);
+            pack(vb, 1, 0);
+            put(1, 0);
           }
           tmem_st_wait();
         }

@@ -99,7 +99,10 @@ class PagePool:
         rp = self._given(rows, "rows", (n,))
         lp = None if new_lens is None else self._given(new_lens, "new_lens", (n,))
         if copy_src is None or copy_dst is None:
-            src, dst = self._new((n, n), stream)
+            src, dst = torch.empty_like(rows), torch.empty_like(rows)
+            if stream is not None:
+                src.record_stream(stream)
+                dst.record_stream(stream)
             sp, dp = src.data_ptr(), dst.data_ptr()
         if copy_src is not None:
             src, sp = copy_src, self._given(copy_src, "copy_src", (n,))
