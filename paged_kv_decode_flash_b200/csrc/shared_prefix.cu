@@ -126,9 +126,9 @@ cudaError_t launch_pdl(void (*kern)(const SharedParams), dim3 grid, const Shared
 SharedPlan make_shared_plan(int num_seqs, int rows_seq, int num_kv_heads, int kv_dtype, int sms) {
   SharedPlan pl;
   pl.rows_head = num_seqs * rows_seq;
-  // 256 rows on a K and a V tile halve the traffic to shared memory; the int8
-  // caches' converted tiles leave room for 128.
-  pl.row_tile = kv_dtype == kKvFp16 && pl.rows_head > 128 ? 256 : 128;
+  // 256 rows on a K and a V tile halve the traffic to shared memory and the
+  // conversions; q8_0's operands, two tiles each, leave room for 128.
+  pl.row_tile = kv_dtype != kKvQ8_0 && pl.rows_head > 128 ? 256 : 128;
   pl.rows_seq = rows_seq;
   pl.parts = (rows_seq + 127) / 128;
   pl.rows_part = (rows_seq + pl.parts - 1) / pl.parts;

@@ -35,8 +35,8 @@
 //   int8 rows: qs enters as it is.  K's row scale multiplies the scores, V's
 //         the weights before their split, so that both cost no MMA; the
 //         row's reference covers the largest |V scale| of a tile, too.
-// They run single segments only: 128 rows leave shared memory for the
-// converted tiles.
+// q8_0 runs single segments only: 128 rows leave shared memory for operands of
+// two tiles.
 //
 // Roles: warps 0-7 the softmax, which also stages Q and writes the partials.
 // Then, fp16: a producer (TMA boxes of 16 keys through the block table);
@@ -75,7 +75,6 @@ constexpr uint32_t kChunkBytes = kChunk * 256;
 // fp16's range cuts off.
 constexpr float kShift = 2.f;
 constexpr float kSumLimit = 32768.f;
-constexpr float kLazy = 13.f;  // int8: a row whose maximum passes its reference by this moves it
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kInvalidLse = 0x7fc00000u;  // NaN: a partial that must not be used
 constexpr int kStep = 64;       // keys of a step of a stream
@@ -107,15 +106,16 @@ template <int KV>
 struct Cfg {
   static constexpr bool kQuant = KV != kKvFp16;
   static constexpr bool kQ8 = KV == kKvQ8_0, kRow = KV == kKvInt8Row;
+  static constexpr bool kDualOk = !kQ8;  // q8_0 operands are two tiles each
   static constexpr int kProdWarp = 8;                      // fp16: producer; int8: converters
   static constexpr int kMmaWarp = kProdWarp + (kQuant ? 8 : 1);  // [2], then the segments' warp
   static constexpr int kReaders = kMmaWarp + 2;            // warps that follow the segments
   static constexpr int kThreads = kQuant ? 640 : 384;
   static constexpr uint32_t kSlot = (kQ8 ? 2 : 1) * kTileBytes;  // q8_0: the high tile, the residual
   static constexpr int KS = kQ8 ? 1 : kRow ? 2 : 3;
-  static constexpr int VS = kRow ? 3 : 2;
+  static constexpr int VS = 2;
   static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = kQ + (kQuant ? 1 : 2) * kTileBytes;
+  static constexpr uint32_t kK = kQ + (kDualOk ? 2 : 1) * kTileBytes;
   static constexpr uint32_t kV = kK + KS * kSlot;
   static constexpr uint32_t kBars = kV + VS * kSlot;
   static constexpr uint32_t kMisc = kBars + (BAR_COUNT * 8 + 15) / 16 * 16;         // int [16], see below
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const SharedParams p) {
   using C = Cfg<KV>;
-  constexpr bool kQuant = C::kQuant, kQ8 = C::kQ8, kRow = C::kRow;
+  constexpr bool kQuant = C::kQuant, kQ8 = C::kQ8, kRow = C::kRow, kDualOk = C::kDualOk;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       if (!ok) return;
       const int gn = __reduce_max_sync(0xffffffffu, g.n);
       const int flags = __reduce_max_sync(0xffffffffu, g.flags);
-      const bool dual = !kQuant && (flags & kDual);
+      const bool dual = kDualOk && (flags & kDual);
       const int Y = dual ? 2 * gn : gn;  // steps of the stream
       const uint64_t q = dQ + ((dual ? w : (flags & kBuf) ? 1 : 0) * kTileBytes >> 4);
       ok = wait1(BAR_QFULL, seg);
@@ -707,8 +707,8 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
         const int st = count % kSegSlots;
         if (!seg_wait(BAR_GEMPTY + st, (count / kSegSlots) ^ 1)) return;
         segs[st] = g;
-        // Q of a single segment: the two buffers in turn (one buffer for int8).
-        buf = kQuant || (g.flags & kDual) ? 0 : buf ^ kBuf;
+        // Q of a single segment: the two buffers in turn (q8_0 has one).
+        buf = !kDualOk || (g.flags & kDual) ? 0 : buf ^ kBuf;
         segs[st].flags |= buf;
         mbar_arrive(bar(BAR_GFULL + st));
         ++count;
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     bool ok = true;
     // Stages this warpgroup's share of a segment's Q rows.
     auto stage_q = [&](const Segment& g) {
-      const bool dual = !kQuant && (g.flags & kDual);
+      const bool dual = kDualOk && (g.flags & kDual);
       const int local = (dual ? w * 128 : 0) + r, row = g.row0 + local;
       const bool in = local < g.nrows;
       const __half* src = p.q + ((long long)(in ? row / p.group : 0) * p.num_q_heads + g.kvh * p.group +
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
     else got = false;
     while (got) {
       const Segment& g = segs[seg % kSegSlots];
-      const bool dual = !kQuant && (g.flags & kDual);
+      const bool dual = kDualOk && (g.flags & kDual);
       const int local = (dual ? w * 128 : 0) + r, row = g.row0 + local;
       const bool mine = local < g.nrows;
       const int tok = row / p.group;  // of all sequences' new tokens
@@ -830,6 +830,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       const bool warp_rows = __any_sync(0xffffffffu, mine);
       float m = -INFINITY, l = 0.f;  // reference (log2 units) and scaled sum
       float bias = 0.f;              // kShift - m, 0 before the first key
+      bool fresh = true;             // int8: some row of the warp is before its first key
       const int Y = dual ? 2 * g.n : g.n;
       // Steps from key wlo to whi need no mask in this warp.
       const int wlo = __reduce_max_sync(0xffffffffu, mine ? max(lo, g.lo) : g.lo);
@@ -951,12 +952,6 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             }
             return true;
           };
-          auto top_of = [&](const float (&v)[32]) -> float {
-            float mx = v[0];
-#pragma unroll
-            for (int e = 1; e < 31; e += 2) mx = max3(mx, v[e], v[e + 1]);
-            return fmaxf(mx, v[31]);
-          };
           // Weights of 32 keys over their scores: 16 columns of high parts, 16
           // of residuals (exact: w - fp16(w) fits fp32).
           constexpr int kPack = kHold ? 16 : 8;  // words of each at a time
@@ -976,32 +971,83 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             tmem_st(tS + c * 32 + 16 + z, pl);
           };
           if constexpr (!kHold) {
-            // Two passes over S in TMEM, 32 columns at a time: the converters
-            // leave no registers for a step's 64 scores.
-            tmem_ld_wait(va);
-            scaled(va, 0);
-            float mx = top_of(va);
-            tmem_ld32(tS + 32, va);
-            tmem_ld_wait(va);
-            scaled(va, 1);
-            mx = fmaxf(mx, top_of(va));
-            const float top = (kRow ? mx : mx * cs) + vtop;
-            const bool raise = mine && top > m + kLazy;
-            if (__any_sync(0xffffffffu, raise) && !move(raise, top)) break;
-            sum = sum2 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            // 32 columns at a time: the converters leave no registers for a
+            // step's 64 scores.  As below, a row keeps its reference while its
+            // sums stay below the limit.
+            auto top_of = [&](int x) -> float {  // the chunk's maximum, read again
               tmem_ld32(tS + x * 32, va);
               tmem_ld_wait(va);
               scaled(va, x);
-              weights(va);
+              float mx = va[0];
+#pragma unroll
+              for (int e = 1; e < 31; e += 2) mx = max3(mx, va[e], va[e + 1]);
+              return (kRow ? fmaxf(mx, va[31]) : fmaxf(mx, va[31]) * cs) + vtop;
+            };
+            auto chunk_weights = [&](int x) -> float {
+              tmem_ld32(tS + x * 32, va);
+              tmem_ld_wait(va);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                float4 k = make_float4(cs, cs, cs, cs);
+                if constexpr (kRow) k = ks[x * 8 + e / 4];
+                const float2 a = fma2(make_float2(va[e], va[e + 1]), make_float2(k.x, k.y), make_float2(bias, bias));
+                const float2 b = fma2(make_float2(va[e + 2], va[e + 3]), make_float2(k.z, k.w), make_float2(bias, bias));
+                va[e] = a.x; va[e + 1] = a.y; va[e + 2] = b.x; va[e + 3] = b.y;
+              }
+              mask(va, x);
+              float2 a = make_float2(0.f, 0.f), b = a;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) va[e + i] = fast_exp2(va[e + i]);
+                a = add2(a, make_float2(va[e], va[e + 1]));
+                b = add2(b, make_float2(va[e + 2], va[e + 3]));
+              }
+              return (a.x + a.y) + (b.x + b.y);
+            };
+            if (fresh) {  // rows at their first keys
+              const float t0 = top_of(0), top = fmaxf(t0, top_of(1));
+              if (!move(mine && m == -INFINITY, top)) break;
+              fresh = __any_sync(0xffffffffu, mine && m == -INFINITY);
+            }
+            const float most = kRow ? fast_exp2(-vtop) * kSumLimit : kSumLimit;
+            bool up = true;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float total = chunk_weights(x);
+              const bool need = mine && m != -INFINITY && !(total <= most);
+              if (__any_sync(0xffffffffu, need)) {
+                const float before = m;
+                up = move(need, top_of(x));
+                if (x == 1 && up) {  // the first chunk's weights, stored already
+                  tmem_ld32(tS, va);
+                  tmem_ld_wait(va);
+                  const float f = fast_exp2(before - m);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const uint32_t h = __float_as_uint(va[i]), r = __float_as_uint(va[16 + i]);
+                    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                    const float2 rf = __half22float2(*reinterpret_cast<const __half2*>(&r));
+                    const float2 w2 = mul2(add2(hf, rf), make_float2(f, f));
+                    const uint32_t nh = h2_bits(__floats2half2_rn(w2.x, w2.y));
+                    const float2 lo2 = residual(w2, nh);
+                    const uint32_t nr = h2_bits(__floats2half2_rn(lo2.x, lo2.y));
+                    va[i] = __uint_as_float(before == m ? h : nh);
+                    va[16 + i] = __uint_as_float(before == m ? r : nr);
+                  }
+                  tmem_st<16>(tS, va);
+                  tmem_st<16, 16>(tS + 16, va);
+                }
+                total = chunk_weights(x);
+              }
+              l += total;
 #pragma unroll
               for (int z = 0; z < 16; z += kPack) {
                 pack(va, x, z);
                 put(x, z);
               }
             }
-            l += (sum.x + sum.y) + (sum2.x + sum2.y);
+            if (!up) break;
           } else {
             auto all_weights = [&]() -> float {
               scaled(va, 0);
@@ -1062,7 +1108,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       // The next segment's Q goes into the other buffer, where there is one.
       const Segment& gn = segs[(seg + 1) % kSegSlots];
       bool more = __all_sync(0xffffffffu, seg_wait(BAR_GFULL + (seg + 1) % kSegSlots, (seg + 1) / kSegSlots));
-      const bool q_ahead = !kQuant && more && gn.n != 0 && !dual && !(gn.flags & kDual);
+      const bool q_ahead = kDualOk && more && gn.n != 0 && !dual && !(gn.flags & kDual);
       if (q_ahead) stage_q(gn);
       ok = __all_sync(0xffffffffu, ok && wait(BAR_SEG, seg));
       bool row_bad = false;
