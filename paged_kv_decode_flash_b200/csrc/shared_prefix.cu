@@ -48,12 +48,19 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
     if (lane == 0) atomicOr(p.flags, kFlagBadLen);
   }
   // The row's partials: np of the prefix, then no of its own keys.
+  // (What a kernel that gave up did not write is not followed.)
   int np = 0, no = 0;
+  bool bad = false;
+  auto count = [&](int2 c) {
+    if (c.x >= 0 && c.x <= c.y && c.y < p.ctas) return c.y - c.x + 1;
+    bad = true;
+    return 0;
+  };
   if (ok) {
-    if (nt > 0) np = cp.y - cp.x + 1;
+    if (nt > 0) np = count(cp);
     int lo, hi;
     union_range(L, p.n_query, p.causal, p.window, lo, hi);
-    if (hi >= max(lo, P)) no = co.y - co.x + 1;
+    if (hi >= max(lo, P)) no = count(co);
   }
   const long long at_p = (long long)(cp.x + gp) * p.row_tile + rh % p.row_tile;
   const long long at_o = p.own_row0 + (long long)(co.x + go) * p.rows_part + rs % p.rows_part;
@@ -61,7 +68,6 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
     return k < np ? at_p + (long long)k * p.row_tile : at_o + (long long)(k - np) * p.rows_part;
   };
   float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
-  bool bad = false;
   for (int k0 = 0; k0 < np + no; k0 += 32) {  // 32 partials at a time, lane k their lse
     const int n = min(32, np + no - k0);
     const float e = lane < n ? __ldcg(p.part_lse + slot(k0 + lane)) : -INFINITY;

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   const int NT = (R + p.row_tile - 1) / p.row_tile;
   const long long Wp = (long long)p.num_kv_heads * uh * nt;
   // A call with a tile for every CTA at most: none gets two.
-  const int start = Wp + (both >> 22) * hp <= p.ctas ? 0 : u1 == 2 ? kOwnStart : kOwnStart / 2;
+  const int start = Wp + (both >> 22) * hp <= p.ctas ? 0 : u1 == 2 && !kQuant ? kOwnStart : kOwnStart / 2;
   auto own_units = [&](long long tiles_and_seqs) {
     return hp * ((tiles_and_seqs >> 22) + start * (tiles_and_seqs & 0x3fffff));
   };
