@@ -106,6 +106,7 @@ struct PageParams {
   void* v_cache;
   long long page_bytes;   // of one cache
   int num_seqs, max_blocks_per_seq, block_size, num_blocks, n;
+  int tables_too;         // compact: the planning kernel rewrites the tables
   unsigned* flags;        // workspace status word
   int* row_scratch;       // [3][num_seqs]
   int* page_scratch;      // [3][num_blocks]

@@ -556,6 +556,28 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_one_kernel(const PageP
 }
 
 // ---------------------------------------------------------------- compact
+// A row's entries after a compaction, by `step` threads of which this is `at`.
+__device__ __forceinline__ void remap_row(const PageParams& p, int row, int at, int step) {
+  const int L = __ldcg(p.context_lens + row);
+  if (!len_ok(p, L)) {
+    if (at == 0) atomicOr(p.flags, kFlagBadLen);
+    return;
+  }
+  const int held = pages_of(p, L);
+  int32_t* t = table_row(p, row);
+#pragma unroll 4
+  for (int b = at; b < held; b += step) {
+    const int page = __ldcg(t + b);
+    if (!page_ok(p, page)) {
+      atomicOr(p.flags, kFlagBadBlock);
+      continue;
+    }
+    const int to = __ldcg(p.remap + page);
+    if (to < 0) atomicOr(p.flags, kFlagBadRequest);  // the row holds a free page
+    else if (to != page) t[b] = to;
+  }
+}
+
 // n_live live pages; the k-th lowest live page at or above n_live moves to
 // the k-th lowest free page below it.
 __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const PageParams p) {
@@ -607,30 +629,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_kernel(const PagePara
     p.copy_dst[k] = -1;
   }
   if (rank == 0 && tid == 0) *p.count = moves;
+  if (!p.tables_too) return;
+  cluster_sync();  // every page's new place is known
+  for (int row = rank * (kPlanThreads / 32) + tid / 32; row < p.num_seqs; row += kPlanAll / 32)
+    remap_row(p, row, tid % 32, 32);
 }
 
 // The tables after a compaction: one CTA per row.
 __global__ void __launch_bounds__(256) remap_kernel(const PageParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int row = blockIdx.x;
-  const int L = __ldcg(p.context_lens + row);
-  if (!len_ok(p, L)) {
-    if (threadIdx.x == 0) atomicOr(p.flags, kFlagBadLen);
-    return;
-  }
-  const int held = pages_of(p, L);
-  int32_t* t = table_row(p, row);
-  for (int b = threadIdx.x; b < held; b += blockDim.x) {
-    const int page = __ldcg(t + b);
-    if (!page_ok(p, page)) {
-      atomicOr(p.flags, kFlagBadBlock);
-      continue;
-    }
-    const int to = __ldcg(p.remap + page);
-    if (to < 0) atomicOr(p.flags, kFlagBadRequest);  // the row holds a free page
-    else if (to != page) t[b] = to;
-  }
+  remap_row(p, blockIdx.x, threadIdx.x, 256);
 }
 
 // ------------------------------------------------------------------- copy
@@ -777,9 +786,15 @@ cudaError_t launch_resize(const PageParams& p, cudaStream_t stream) {
   }
   return launch(resize_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
 }
-cudaError_t launch_compact(const PageParams& p, cudaStream_t stream) {
+// Tables of up to this many entries are rewritten by the planning cluster
+// itself; larger ones by a launch over all SMs (184,000 entries: 4 us).
+constexpr long long kTablesInside = 32768;
+
+cudaError_t launch_compact(const PageParams& params, cudaStream_t stream) {
+  PageParams p = params;
+  p.tables_too = (long long)p.num_seqs * p.max_blocks_per_seq <= kTablesInside;
   const cudaError_t e = launch(compact_kernel, kPlanCtas, kPlanThreads, kPlanCtas, p, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.tables_too) return e;
   return launch(remap_kernel, p.num_seqs, 256, 1, p, stream);
 }
 cudaError_t launch_copy_blocks(const PageParams& p, int sms, cudaStream_t stream) {

@@ -47,6 +47,8 @@ class PagePool:
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         self.device = device
+        self._caches = {kv: _b.cache_shape(kv, num_blocks, num_kv_heads, block_size, head_dim)
+                        for kv in (_b.KV_FP16, _b.KV_Q8_0, _b.KV_INT8_ROW)}
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
         elif workspace.numel() * workspace.element_size() < need:
@@ -129,15 +131,17 @@ class PagePool:
     def copy(self, k_cache, v_cache, src, dst, *, kv_dtype: int, count=None, stream=None) -> None:
         """paged_attn_copy_blocks on one layer's caches: page dst[i] becomes a
         copy of page src[i] (negative src: skipped)."""
-        d = self.dims
-        dtype, shape = _b.cache_shape(kv_dtype, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+        kind = self._caches.get(kv_dtype)
+        if kind is None:
+            _b.cache_shape(kv_dtype, 1, 1, 16, 128)  # raises
+        dtype, shape = kind
         kp = _b._given(k_cache, "k_cache", dtype, shape, self.device)
         vp = _b._given(v_cache, "v_cache", dtype, shape, self.device)
         n = src.numel()
         sp, dp = self._given(src, "src", (n,)), self._given(dst, "dst", (n,))
         cp = None if count is None else self._given(count, "count", (1,))
         _b._check(_b._on(self.device.index, stream, lambda st: _b.lib().paged_attn_copy_blocks(
-            d, sp, dp, n, cp, int(kv_dtype), kp, vp, st)), "paged_attn_copy_blocks")
+            self.dims, sp, dp, n, cp, kv_dtype, kp, vp, st)), "paged_attn_copy_blocks")
 
     def get_error(self, stream=None) -> int:
         """Synchronises and returns (and clears) what the device refused."""

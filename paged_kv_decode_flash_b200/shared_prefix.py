@@ -38,6 +38,8 @@ class SharedPrefixDecode(_b.PagedDecode):
                              n_query=n_query, workspace=workspace)
         self.workspace_bytes = need
         self.prefix_blocks = int(prefix_blocks)
+        self._caches = {kv: _b.cache_shape(kv, num_blocks, num_kv_heads, block_size, head_dim)
+                        for kv in (_b.KV_FP16, _b.KV_Q8_0, _b.KV_INT8_ROW)}
 
     @classmethod
     def for_case(cls, case, prefix_blocks, device=None):
@@ -65,7 +67,10 @@ class SharedPrefixDecode(_b.PagedDecode):
                                     stream=stream)
         d, dev = self.dims, self.workspace.device
         qshape = (d.num_seqs, self.n_query, d.num_q_heads, d.head_dim)
-        dtype, shape = _b.cache_shape(kv_dtype, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+        kind = self._caches.get(kv_dtype)
+        if kind is None:
+            _b.cache_shape(kv_dtype, 1, 1, 16, 128)  # raises
+        dtype, shape = kind
         args = (_b._given(q, "q", torch.float16, qshape, dev),
                 _b._given(k_cache, "k_cache", dtype, shape, dev),
                 _b._given(v_cache, "v_cache", dtype, shape, dev),
