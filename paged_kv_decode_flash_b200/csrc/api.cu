@@ -57,7 +57,10 @@ int check_shared(const pa_dims* d, int n_query, int prefix_blocks) {
   const int rc = check_dims(d, n_query);
   if (rc != PA_OK) return rc;
   if (prefix_blocks < 1) return PA_ERR_INVALID_ARG;
-  if ((long long)prefix_blocks * d->block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  // Keys are numbered in ints, up to a tile's end behind the last one.
+  if ((long long)prefix_blocks * d->block_size > INT32_MAX - 256 ||
+      (long long)d->max_blocks_per_seq * d->block_size > INT32_MAX - 256)
+    return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 

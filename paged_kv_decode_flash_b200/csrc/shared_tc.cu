@@ -8,12 +8,13 @@
 // keys; the partial is O / l with lse = (m - 2 + log2 l) ln 2.
 //
 // Work.  Prefix: the rows of a KV head (sequences x new tokens x the head's
-// query heads) are cut into row tiles, 256 rows (fp16) or 128; a (KV head,
-// row tile) is a group.  Own keys: a (sequence, KV head, part of at most 128
+// query heads) are cut into row tiles of 256 rows (128 where there are no
+// more, and for q8_0); a (KV head, row tile) is a group.  Own keys: a (sequence, KV head, part of at most 128
 // of the sequence's rows) is a group.  A group's visible keys are numbered in
 // tiles of 128.  The tiles of all groups, prefix first, are laid end to end
-// (WorkCut below) and cut into equal ranges over the CTAs (one per SM); a
-// CTA's run of tiles of one group is a segment and makes one partial per row.
+// and cut into equal ranges over the CTAs (one per SM; an own group's start
+// counts as a few tiles); a CTA's run of tiles of one group is a segment and
+// makes one partial per row.
 //
 // A CTA has two streams, each a softmax warpgroup (thread = query row) and an
 // O accumulator of 128 x 128 in TMEM:
@@ -44,6 +45,19 @@
 // an MMA issuer for each stream (one for both was the bottleneck: with the
 // waits, a step's sixteen products take a warp 1750 cycles to issue and the
 // tensor cores 780), and a warp that cuts the CTA's range into segments.
+//
+// Bounds.  Many rows: the tensor cores.  A step's products take 8 x 49 cycles
+// (Q K^T with N = 64: Q and K come from shared memory, 6 KB a product) and
+// 8 x 64 (P V), 1808 for both streams; a pair of steps was measured at 2210
+// (512 rows a KV head, 8 of them, 131072 keys: 392 us), 2366 with the commits
+// between the products and V awaited behind P, 4800 with one issuer that is one
+// lane.  The exponentials (2 x 64 a lane, 1024 cycles) and the conversions
+// to fp16 share what is left.  q8_0: 4400 a pair, int8 rows 3440, set by the
+// converters and the softmax together (48% of the issue slots).  Few rows: a
+// chain of latencies, 4.1 us to the first scores, 8 to the end of a segment
+// of one tile.  Tried without gain: the streams' exponentials in turn, half a
+// step's keys a warp (four softmax warps a scheduler), the scores of both
+// streams of a single segment in one product of N = 128, q8_0 slots of 64 keys.
 //
 // Every wait is bounded (SharedParams::wait_limit_ns): on a timeout the
 // kernel raises kFlagTimeout, drains its copies and MMAs with a fixed bound,

@@ -141,7 +141,7 @@ class PagePool:
         sp, dp = self._given(src, "src", (n,)), self._given(dst, "dst", (n,))
         cp = None if count is None else self._given(count, "count", (1,))
         _b._check(_b._on(self.device.index, stream, lambda st: _b.lib().paged_attn_copy_blocks(
-            self.dims, sp, dp, n, cp, kv_dtype, kp, vp, st)), "paged_attn_copy_blocks")
+            self.dims, sp, dp, n, cp, int(kv_dtype), kp, vp, st)), "paged_attn_copy_blocks")
 
     def get_error(self, stream=None) -> int:
         """Synchronises and returns (and clears) what the device refused."""

@@ -56,6 +56,16 @@ def test_a_plan_never_outgrows_the_workspace():
             last = n
 
 
+def test_lengths_at_the_end_of_the_int_range_are_refused():
+    import ctypes
+    from paged_kv_decode_flash_b200 import binding as b, build
+    build.build()
+    for entries, blocks, ok in (((1 << 31) // 16 - 17, 4, True), ((1 << 31) // 16 - 1, 4, False),
+                                (4, (1 << 31) // 16 - 17, True), (4, (1 << 31) // 16 - 1, False)):
+        d = b.Dims(1, 8, 2, 128, 16, entries, 1000, None, 0)
+        assert (b.lib().paged_attn_shared_workspace_size(ctypes.byref(d), 1, blocks) > 0) == ok
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("nseq,prefix", [(385, 320), (641, 0), (1500, 96)])
