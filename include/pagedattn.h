@@ -184,7 +184,8 @@ int paged_attn_decode_partial(const pa_dims* dims, const void* q, const void* k_
  * paged_attn_decode's (another order of the sums); repeated calls give
  * bit-identical results, and a sequence's result does not depend on the
  * finite values of the others (a value that is not finite, in a prefix key
- * that some row sees, may reach every row).  The workspace must have
+ * that some row sees, may reach every row); a row with a score of NaN or
+ * +infinity is NaN.  The workspace must have
  * paged_attn_shared_workspace_size bytes, be initialised by
  * paged_attn_workspace_init and may serve paged_attn_decode calls too. */
 int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_cache,

@@ -22,7 +22,8 @@ constexpr int kJoin = 8;  // partials loaded at a time
 
 // The join: one warp per output row over the row's partials, weights
 // e^(lse - max).  A NaN log-sum-exp (an out-of-range block, a timeout) and a
-// bad length give a row of zeros.
+// bad length give a row of zeros, one of +inf (a score that is not finite) a
+// row of NaN.
 __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) {
   const int lane = threadIdx.x % 32;
   const long long rows = (long long)p.num_seqs * p.n_query * p.num_q_heads;
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
   // The row's partials: np of the prefix, then no of its own keys.
   // (What a kernel that gave up did not write is not followed.)
   int np = 0, no = 0;
-  bool bad = false;
+  bool bad = false, odd = false;
   auto count = [&](int2 c) {
     if (c.x >= 0 && c.x <= c.y && c.y < p.ctas) return c.y - c.x + 1;
     bad = true;
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
                          : make_float4(0.f, 0.f, 0.f, 0.f);
       if (k == 0) {
         bad |= __any_sync(0xffffffffu, isnan(e));
+        odd |= __any_sync(0xffffffffu, e == INFINITY);
         mx = fmaxf(e, M);
 #pragma unroll
         for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -103,8 +105,8 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
       }
     }
   }
-  const float inv = l > 0.f && !bad ? 1.f / l : 0.f;
-  auto end = [&](float x) { return inv > 0.f ? x * inv : 0.f; };
+  const float inv = bad ? 0.f : odd ? __uint_as_float(0x7fc00000u) : l > 0.f ? 1.f / l : 0.f;
+  auto end = [&](float x) { return inv != 0.f ? x * inv : 0.f; };
   const __half2 a = __floats2half2_rn(end(o[0]), end(o[1]));
   const __half2 b = __floats2half2_rn(end(o[2]), end(o[3]));
   uint2 u;

@@ -9,12 +9,12 @@
 //
 // Work.  Prefix: the rows of a KV head (sequences x new tokens x the head's
 // query heads) are cut into row tiles of 256 rows (128 where there are no
-// more, and for q8_0); a (KV head, row tile) is a group.  Own keys: a (sequence, KV head, part of at most 128
-// of the sequence's rows) is a group.  A group's visible keys are numbered in
-// tiles of 128.  The tiles of all groups, prefix first, are laid end to end
-// and cut into equal ranges over the CTAs (one per SM; an own group's start
-// counts as a few tiles); a CTA's run of tiles of one group is a segment and
-// makes one partial per row.
+// more, and for q8_0); a (KV head, row tile) is a group.  Own keys: a
+// (sequence, KV head, part of at most 128 of the sequence's rows) is a group.
+// A group's visible keys are numbered in tiles of 128.  The tiles of all
+// groups, prefix first, are laid end to end and cut into equal ranges over the
+// CTAs (one per SM; an own group's start counts as a few tiles); a CTA's run
+// of tiles of one group is a segment and makes one partial per row.
 //
 // A CTA has two streams, each a softmax warpgroup (thread = query row) and an
 // O accumulator of 128 x 128 in TMEM:
@@ -61,7 +61,8 @@
 //
 // Every wait is bounded (SharedParams::wait_limit_ns): on a timeout the
 // kernel raises kFlagTimeout, drains its copies and MMAs with a fixed bound,
-// frees TMEM and marks its partials (NaN lse; the join writes zeros).
+// frees TMEM and marks its partials (NaN lse; the join writes zeros).  An lse
+// of +inf marks a row with a score of NaN or +inf (the join writes NaN).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + C::kQ, sK = sbase + C::kK, sV = sbase + C::kV;
-    // [0] TMEM base, [1] abort, [2] shortest sequence, [3] start sequence,
+  // [0] TMEM base, [1] abort, [2] shortest sequence, [3] start sequence,
   // [4, 5] its start, [6, 7] own tiles and sequences behind the first round, [8] segments given up,
   // [9] a block was out of range
   int* misc = reinterpret_cast<int*>(smem + C::kMisc);
@@ -992,10 +993,10 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               tmem_ld32(tS + x * 32, va);
               tmem_ld_wait(va);
               scaled(va, x);
-              float mx = va[0];
+              float mx = -INFINITY;  // (scores of NaN are passed over)
 #pragma unroll
-              for (int e = 1; e < 31; e += 2) mx = max3(mx, va[e], va[e + 1]);
-              return (kRow ? fmaxf(mx, va[31]) : fmaxf(mx, va[31]) * cs) + vtop;
+              for (int e = 0; e < 32; e += 2) mx = max3(mx, va[e], va[e + 1]);
+              return (kRow ? mx : mx * cs) + vtop;
             };
             auto chunk_weights = [&](int x) -> float {
               tmem_ld32(tS + x * 32, va);
@@ -1146,15 +1147,16 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       const float2 s1 = dual ? make_float2(-INFINITY, 0.f) : stat[128 + r];
       more = named_bar_and(2, kSoftThreads, more);  // (the same for all)
       // single: the two streams' sums; f0, f1: the accumulators' factors
-      const bool bad = !ok || isnan(s0.x + s0.y) || isnan(s1.x + s1.y);
+      const bool bad = !ok || isnan(s0.x) || isnan(s1.x);
       const float mm = fmaxf(s0.x, s1.x);
       const float w0 = s0.y > 0.f ? fast_exp2(s0.x - mm) : 0.f;
       const float w1 = s1.y > 0.f ? fast_exp2(s1.x - mm) : 0.f;
       const float ll = s0.y * w0 + s1.y * w1;
       if ((dual || w == 0) && mine)
-        p.part_lse[g.out_row + local] = bad        ? __uint_as_float(kInvalidLse)
-                                        : ll > 0.f ? (mm - kShift + log2f(ll)) * kLn2
-                                                   : -INFINITY;
+        p.part_lse[g.out_row + local] = bad         ? __uint_as_float(kInvalidLse)
+                                        : ll > 0.f  ? (mm - kShift + log2f(ll)) * kLn2
+                                        : ll == 0.f ? -INFINITY
+                                                    : INFINITY;  // a score was not finite
       if (ok && warp_rows) {
         tc_fence_after();
         const float inv = ll > 0.f ? 1.f / ll : 0.f;

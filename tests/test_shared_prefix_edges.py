@@ -146,6 +146,53 @@ def test_references_that_rise_all_the_way(S, orc, dt, own, top):
     assert_parity(TS.run(S, case, PREFIX), ref, "rising")
 
 
+def poison_key(case, seq, key, head):
+    """NaN in the key (not the value) of one position of one KV head."""
+    block, slot = case.block_table[seq, key // case.block_size], key % case.block_size
+    if case.kv_dtype == gen.KV_FP16:
+        case.k_cache[block, head, slot, :] = np.float16(np.nan)
+    else:
+        width = 8 if case.kv_dtype == gen.KV_Q8_0 else 4
+        nan = np.full(4, np.nan, np.float16) if width == 8 else np.full(1, np.nan, np.float32)
+        at = case.block_size * 128 + slot * width
+        case.k_cache[block, head, at: at + width] = nan.view(np.uint8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("G,own", [(4, (5, 40, 9)), (8, (7,) * 20)])
+def test_scores_that_are_not_finite_show(S, orc, dt, G, own):
+    """A row that sees a NaN key, or whose query holds one, is NaN, as the
+    formula has it, and no other row is touched."""
+    prefix, nq = 640, 3
+    case = TS.shared_case(prefix, own, n_query=nq, num_q_heads=2 * G, num_kv_heads=2, kv_dtype=dt)
+    ref, _ = orc.attend(case)
+    ref = np.asarray(ref)
+    dec, args, kw = TS.prepared(S, case, prefix)
+    shape = dec(*args, **kw).shape
+    assert shape == ref.shape == (len(own), nq, 2 * G, 128)
+
+    def check(nan, what):
+        out = TS.run(S, case, prefix)
+        assert np.isnan(out[nan]).all(), what
+        assert_parity(out[~nan], ref[~nan], what)
+
+    nan = np.zeros((len(own), nq, 2 * G), bool)
+    L = prefix + own[1]
+    poison_key(case, 1, L - 2, 0)  # seen by the last two of sequence 1's new tokens
+    nan[1, 1:, :G] = True
+    check(nan, "own key")
+    case.q[0, 0, 2 * G - 1, 5] = np.float16(np.nan)
+    nan[0, 0, 2 * G - 1] = True
+    check(nan, "query")
+    case.q[2, 2, 0, :] = np.float16(np.inf)
+    nan[2, 2, 0] = True
+    check(nan, "infinite query")
+    poison_key(case, 0, 70, 1)  # seen by every row of its KV head
+    nan[:, :, G:] = True
+    check(nan, "prefix key")
+
+
 @pytest.mark.gpu
 def test_row_scales_of_every_size(S, orc):
     """int8 rows whose scales lie 80 powers of two apart, key by key: V's are
