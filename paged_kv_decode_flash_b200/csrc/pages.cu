@@ -691,7 +691,7 @@ constexpr int kCopyVecs = 4;                                  // 16-byte vectors
 constexpr int kCopyPiece = kCopyThreads * kCopyVecs * 16;     // bytes per work unit
 // Up to this many pairs every CTA looks its own ones over against the list
 // (eight entries a thread): no launch and no cluster barriers before the
-// copies, 5.1 us instead of 6.1 for 7 pairs (with host time 10 instead of 16).
+// copies, 5.1 us instead of 6.1 for 7 pairs, and one launch less on the host.
 constexpr int kCopySelfCheck = 2048;
 
 // Persistent: units (pair, K or V, piece of a page) over the grid.

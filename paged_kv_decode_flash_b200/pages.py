@@ -53,6 +53,8 @@ class PagePool:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
         elif workspace.numel() * workspace.element_size() < need:
             raise _b.PagedAttnError(_b.PA_ERR_WORKSPACE, "workspace too small")
+        elif workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
         books = {"block_table": ((num_seqs, max_blocks_per_seq), block_table, -1),
                  "context_lens": ((num_seqs,), context_lens, 0),
                  "ref_counts": ((num_blocks,), ref_counts, 0)}

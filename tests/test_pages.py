@@ -206,6 +206,13 @@ def test_refusals_on_the_host(L):
         assert L.paged_attn_status_string(code) != b"unknown status"
 
 
+def test_a_workspace_elsewhere_is_refused(L):
+    from paged_kv_decode_flash_b200 import pages
+    with pytest.raises(ValueError, match="workspace"):
+        pages.PagePool(num_seqs=3, num_kv_heads=1, head_dim=128, block_size=16, max_blocks_per_seq=4,
+                       num_blocks=20, device="cuda:0", workspace=torch.empty(4096, dtype=torch.uint8))
+
+
 # ---------------------------------------------------------------------------
 # on the GPU
 # ---------------------------------------------------------------------------
