@@ -13,8 +13,8 @@
 // (sequence, KV head, part of at most 128 of the sequence's rows) is a group.
 // A group's visible keys are numbered in tiles of 128.  The tiles of all
 // groups, prefix first, are laid end to end and cut into equal ranges over the
-// CTAs (one per SM; an own group's start counts as a few tiles); a CTA's run
-// of tiles of one group is a segment and makes one partial per row.
+// CTAs (one per SM; a group's start counts as a few tiles); a CTA's run of
+// tiles of one group is a segment and makes one partial per row.
 //
 // A CTA has two streams, each a softmax warpgroup (thread = query row) and an
 // O accumulator of 128 x 128 in TMEM:
@@ -93,9 +93,11 @@ constexpr float kSumLimit = 32768.f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr unsigned kInvalidLse = 0x7fc00000u;  // NaN: a partial that must not be used
 constexpr int kStep = 64;       // keys of a step of a stream
-// What the start of an own-keys segment costs (5 us), in units: 1.4 us each where
-// two of them are a dual segment's tile, else 2 to 2.5 us.
-constexpr int kOwnStart = 4;
+// What the start of a segment costs (5 us), in units: 1.4 us each where two of
+// them are a dual segment's tile, else 2 to 2.5 us.  (Not weighed for the
+// prefix, 32 sequences behind 16 keys took 47 us: one CTA had five of the eight
+// heads' segments.)
+constexpr int kStart = 4;
 constexpr int kScaleSlots = 8;  // tiles whose row scales are kept: more than are in flight
 
 constexpr int kSegSlots = 4;
@@ -285,9 +287,9 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   __syncthreads();
 
   // ---- the work cut ---------------------------------------------------------
-  // A unit is the product of 128 rows and 128 keys.  Prefix groups: tiles of
-  // one or two (dual) units; own groups: kOwnStart units for the start of a
-  // segment, then tiles of one.  CTA c has the tiles that begin in units
+  // A unit is the product of 128 rows and 128 keys.  A group: `start` units for
+  // the start of a segment, then its tiles, of two units in a dual group of the
+  // prefix, else of one.  CTA c has the tiles that begin in units
   // [c W / Ce, (c + 1) W / Ce).
   auto own_keys = [&](int L, int& lo, int& hi) {  // of all of a sequence's rows
     lo = 0;
@@ -351,9 +353,10 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
   const int u1 = p.row_tile / 128;                          // units of a full row tile's key tile
   const int uh = (R + 127) / 128;                           // ... of all row tiles of a head
   const int NT = (R + p.row_tile - 1) / p.row_tile;
-  const long long Wp = (long long)p.num_kv_heads * uh * nt;
+  const long long tiles_p = (long long)p.num_kv_heads * uh * nt;
   // A call with a tile for every CTA at most: none gets two.
-  const int start = Wp + (both >> 22) * hp <= p.ctas ? 0 : u1 == 2 && !kQuant ? kOwnStart : kOwnStart / 2;
+  const int start = tiles_p + (both >> 22) * hp <= p.ctas ? 0 : u1 == 2 && !kQuant ? kStart : kStart / 2;
+  const long long Wp = nt > 0 ? tiles_p + (long long)p.num_kv_heads * NT * start : 0;
   auto own_units = [&](long long tiles_and_seqs) {
     return hp * ((tiles_and_seqs >> 22) + start * (tiles_and_seqs & 0x3fffff));
   };
@@ -731,15 +734,15 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       long long x = a;
       while (x < b && x < Wp) {
         Segment g;
-        const long long head = (long long)uh * nt, tile = (long long)u1 * nt;
+        const long long head = (long long)uh * nt + NT * start, tile = (long long)u1 * nt + start;
         g.kvh = (int)div_pos(x, head);
         const int i = (int)div_pos(x - g.kvh * head, tile);
-        const long long at = g.kvh * head + i * tile;
+        const long long st = g.kvh * head + i * tile + start;  // unit of the first tile
         g.row0 = i * p.row_tile;
         g.nrows = min(R - g.row0, p.row_tile);
         const int u = g.nrows > 128 ? 2 : 1, u_log = u - 1;
-        g.t0 = (int)((x - at + u - 1) >> u_log);
-        const int te = (int)min((long long)nt, (b - at + u - 1) >> u_log);
+        g.t0 = (int)max(0LL, (x - st + u - 1) >> u_log);
+        const int te = (int)min((long long)nt, (b - st + u - 1) >> u_log);
         g.n = te - g.t0;
         g.table = p.prefix_table;
         g.lo = vlo;
@@ -751,7 +754,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
         g.out_row = (long long)(cta + g.group) * p.row_tile;
         g.flags = (u == 2 ? kDual : 0) | (g.t0 == 0 ? kFirst : 0) | (te == nt ? kLast : 0);
         if (g.n > 0) publish(g);
-        x = at + (long long)u * nt;
+        x = st + (long long)u * nt;
       }
       long long at = *reinterpret_cast<volatile long long*>(misc + 4);  // where sequence s begins
       for (int s = misc[3]; x < b && s < p.num_seqs; ++s) {
