@@ -101,6 +101,17 @@ def test_sequences_with_many_rows(S, orc, dt, nq, G, own):
     TS.check(S, orc, case, 480, "row parts")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("nseq,G,prefix", [(32, 4, 16), (64, 4, 144), (67, 5, 272), (40, 4, 1040)])
+def test_short_prefixes_under_many_sequences(S, orc, dt, nseq, G, prefix):
+    """The starts of segments are most of the work: row tiles of 128 and 256
+    rows (a last one of 79), one to nine tiles of the prefix."""
+    own = [1 + (s * 37) % 150 for s in range(nseq)]
+    case = TS.shared_case(prefix, own, seed=nseq, num_q_heads=8 * G, num_kv_heads=8, kv_dtype=dt)
+    TS.check(S, orc, case, prefix, "short prefix")
+
+
 def ramp(case, prefix, top):
     """Keys that grow along the prefix: every later tile has larger scores.
     Values above 0.5: with scores up to 1400 (log2 units) their fp32 sums are
