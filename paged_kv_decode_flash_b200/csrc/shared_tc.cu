@@ -1201,12 +1201,14 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           __syncwarp();
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BAR_OEMPTY));
       T0 += g.n;
       c0 += Y;
-      if (lane == 0) mbar_arrive(bar(BAR_GEMPTY + seg % kSegSlots));
+      tc_fence_before();
+      __syncwarp();  // no lane reads g any more: its slot is given back
+      if (lane == 0) {
+        mbar_arrive(bar(BAR_OEMPTY));
+        mbar_arrive(bar(BAR_GEMPTY + seg % kSegSlots));
+      }
       ++seg;
       named_bar_sync(3, kSoftThreads);  // this segment's buffer may be staged again
       got = more && gn.n != 0;
