@@ -1038,6 +1038,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
                 const float before = m;
                 up = move(need, top_of(x));
                 if (x == 1 && up) {  // the first chunk's weights, stored already
+                  tmem_st_wait();    // (the stores may still be under way)
                   tmem_ld32(tS, va);
                   tmem_ld_wait(va);
                   const float f = fast_exp2(before - m);
