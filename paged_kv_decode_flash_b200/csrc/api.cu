@@ -36,10 +36,10 @@ int prepare_decode(const pa_dims* dims, const void* q, const void* k_cache, cons
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace of a shared-prefix call: the decode layout (any device, so that
-// the offsets behind it are the same everywhere), the groups' CTAs, the
-// partials.
+// the offsets behind it are the same everywhere), the groups' CTAs, which CTAs
+// gave up, the partials.
 struct SharedWs {
-  size_t meta, part_lse, part_out, total;
+  size_t meta, gave_up, part_lse, part_out, total;
 };
 SharedPlan shared_plan(const pa_dims* d, int n_query, int kv_dtype, int sms) {
   return make_shared_plan(d->num_seqs, n_query * (d->num_q_heads / d->num_kv_heads), d->num_kv_heads,
@@ -48,7 +48,8 @@ SharedPlan shared_plan(const pa_dims* d, int n_query, int kv_dtype, int sms) {
 SharedWs shared_ws(const pa_dims* d, int n_query, const SharedPlan& pl) {
   SharedWs w;
   w.meta = align256(ws_size_any_device(d, n_query));
-  w.part_lse = w.meta + align256((size_t)(1 + pl.groups) * 2 * sizeof(int));
+  w.gave_up = w.meta + align256((size_t)(1 + pl.groups) * 2 * sizeof(int));
+  w.part_lse = w.gave_up + align256(kMaxPrefixCtas * sizeof(int));
   w.part_out = w.part_lse + align256((size_t)pl.part_rows * sizeof(float));
   w.total = w.part_out + (size_t)pl.part_rows * kHeadDim * sizeof(float);
   return w;
@@ -254,6 +255,7 @@ int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_c
   p.part_out = reinterpret_cast<float*>(ws + w.part_out);
   p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   p.meta = reinterpret_cast<int*>(ws + w.meta);
+  p.gave_up = reinterpret_cast<int*>(ws + w.gave_up);
   p.flags = reinterpret_cast<unsigned*>(ws);
   p.out = static_cast<__half*>(out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -76,6 +76,7 @@ struct SharedParams {
   float* part_out;              // partials [slots][row_tile][D], [own slots][rows_part][D]
   float* part_lse;              // natural log
   int* meta;                    // key tiles of the prefix, -; first and last CTA of every group
+  int* gave_up;                 // [ctas] a CTA's waits ran out: its partials are not used
   unsigned* flags;              // workspace status word
   __half* out;                  // [B][nq][Hq][D]
 };

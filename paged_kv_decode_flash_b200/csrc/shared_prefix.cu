@@ -21,9 +21,9 @@ using namespace sm100;
 constexpr int kJoin = 16;  // partials loaded at a time: 18 a row (32 x 4 rows behind 16384 keys), 2.5 us less than by 8
 
 // The join: one warp per output row over the row's partials, weights
-// e^(lse - max).  A NaN log-sum-exp (an out-of-range block, a timeout) and a
-// bad length give a row of zeros, one of +inf (a score that is not finite) a
-// row of NaN.
+// e^(lse - max).  A NaN log-sum-exp (an out-of-range block), a partial of a CTA
+// that gave up and a bad length give a row of zeros, a log-sum-exp of +inf (a
+// score that is not finite) a row of NaN.
 __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) {
   const int lane = threadIdx.x % 32;
   const long long rows = (long long)p.num_seqs * p.n_query * p.num_q_heads;
@@ -49,7 +49,6 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
     if (lane == 0) atomicOr(p.flags, kFlagBadLen);
   }
   // The row's partials: np of the prefix, then no of its own keys.
-  // (What a kernel that gave up did not write is not followed.)
   int np = 0, no = 0;
   bool bad = false, odd = false;
   auto count = [&](int2 c) {
@@ -71,7 +70,12 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedParams p) 
   float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, M = -INFINITY;
   for (int k0 = 0; k0 < np + no; k0 += 32) {  // 32 partials at a time, lane k their lse
     const int n = min(32, np + no - k0);
-    const float e = lane < n ? __ldcg(p.part_lse + slot(k0 + lane)) : -INFINITY;
+    float e = -INFINITY;
+    if (lane < n) {
+      const int k = k0 + lane, late = __ldcg(p.gave_up + (k < np ? cp.x + k : co.x + k - np));
+      e = __ldcg(p.part_lse + slot(k));
+      if (late != 0) e = __uint_as_float(0x7fc00000u);  // what lies there may be another call's
+    }
     float mx = 0.f, we = 0.f;
     for (int k = 0; k < n; k += kJoin) {  // the first ones are loaded beside the lse
       float4 v[kJoin];

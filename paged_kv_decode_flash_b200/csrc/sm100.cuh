@@ -100,6 +100,26 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same where the limit must be kept: try_wait may suspend the thread for a
+// time that the hardware chooses, with the hint, too (a hint of 1 ns outlasted
+// every wait of a kernel of 100 us), so that a limit below the usual hint is
+// watched without it.
+__device__ __forceinline__ bool mbar_wait_strict(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                 unsigned long long limit_ns) {
+  constexpr uint32_t kHint = 20000;
+  const bool poll = limit_ns < kHint;
+  if (!poll && mbar_try_wait_ns(bar, parity, kHint)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (poll ? mbar_test_wait(bar, parity) : mbar_try_wait_ns(bar, parity, kHint)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // Load with acquire semantics at GPU scope (pairs with a release or a fence
 // before another CTA's atomic).
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
