@@ -131,6 +131,20 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _outputs(stream, *makes):
+    """The tensors that `makes` allocate, for work on `stream` (None: the
+    current one).  They come from that stream's memory: a block that the
+    current stream has freed may still be in use by what is queued there."""
+    current = None if stream is None else torch.cuda.current_stream(stream.device)
+    if stream is None or stream == current:
+        return [make() for make in makes]
+    with torch.cuda.stream(stream):
+        made = [make() for make in makes]
+    for t in made:
+        t.record_stream(current)  # the caller may use them there, too
+    return made
+
+
 def _on(index: int, stream, call):
     """call(stream pointer) with device `index` current; stream None: its
     current one."""
@@ -266,7 +280,7 @@ class PagedDecode:
                  window: int, scale: float, kv_dtype: int, out=None, stream=None):
         self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
         if out is None:
-            out = torch.empty_like(q)
+            out, = _outputs(stream, lambda: torch.empty_like(q))
         rc = lib().paged_attn_decode(
             ctypes.byref(self.dims), _dptr(q), _dptr(k_cache), _dptr(v_cache),
             _dptr(block_table), _dptr(context_lens), self.n_query, int(causal), int(window),
@@ -287,9 +301,10 @@ class PagedDecode:
         _expect(key_count, "key_count", torch.int32, (B,))
         shp = tuple(q.shape)
         if out is None:
-            out = torch.empty(shp, dtype=torch.float32, device=q.device)
+            out, = _outputs(stream, lambda: torch.empty(shp, dtype=torch.float32, device=q.device))
         if out_lse is None:
-            out_lse = torch.empty(shp[:-1], dtype=torch.float32, device=q.device)
+            out_lse, = _outputs(stream, lambda: torch.empty(shp[:-1], dtype=torch.float32,
+                                                            device=q.device))
         _expect(out, "out", torch.float32, shp)
         _expect(out_lse, "out_lse", torch.float32, shp[:-1])
         rc = lib().paged_attn_decode_partial(
@@ -310,9 +325,10 @@ class PagedDecode:
         kernel that read the cache.  Returns (out, trace int32 [B][nq][Hq][5])."""
         self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
         if out is None:
-            out = torch.empty_like(q)
+            out, = _outputs(stream, lambda: torch.empty_like(q))
         B, nq, Hq = self.dims.num_seqs, self.n_query, self.dims.num_q_heads
-        t = torch.empty((B, nq, Hq, 5), dtype=torch.int32, device=q.device)
+        t, = _outputs(stream, lambda: torch.empty((B, nq, Hq, 5), dtype=torch.int32,
+                                                  device=q.device))
         rc = lib().paged_attn_trace(
             ctypes.byref(self.dims), _dptr(q), _dptr(k_cache), _dptr(v_cache),
             _dptr(block_table), _dptr(context_lens), nq, int(causal), int(window),
@@ -353,9 +369,11 @@ def merge(partial_out: torch.Tensor, partial_lse: torch.Tensor, out=None, out_ls
     if out_lse is not None:
         _expect(out_lse, "out_lse", torch.float32, (rows,))
     if out is None:
-        out = torch.empty((rows, D), dtype=torch.float16, device=partial_out.device)
+        out, = _outputs(stream, lambda: torch.empty((rows, D), dtype=torch.float16,
+                                                    device=partial_out.device))
     if out_lse is None:
-        out_lse = torch.empty((rows,), dtype=torch.float32, device=partial_out.device)
+        out_lse, = _outputs(stream, lambda: torch.empty((rows,), dtype=torch.float32,
+                                                        device=partial_out.device))
     rc = lib().paged_attn_merge(_dptr(partial_out), _dptr(partial_lse), S, rows, D,
                                 _dptr(out), _dptr(out_lse), _stream_ptr(stream))
     _check(rc, "paged_attn_merge")

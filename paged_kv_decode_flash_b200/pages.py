@@ -81,9 +81,8 @@ class PagePool:
 
     def _new(self, sizes, stream):
         """int32 tensors of these sizes, in one allocation."""
-        t = torch.empty(sum(sizes), dtype=torch.int32, device=self.device)
-        if stream is not None:
-            t.record_stream(stream)
+        t, = _b._outputs(stream, lambda: torch.empty(sum(sizes), dtype=torch.int32,
+                                                     device=self.device))
         return t.split(sizes)
 
     def fork(self, parents, children, *, stream=None) -> None:
@@ -103,10 +102,7 @@ class PagePool:
         rp = self._given(rows, "rows", (n,))
         lp = None if new_lens is None else self._given(new_lens, "new_lens", (n,))
         if copy_src is None or copy_dst is None:
-            src, dst = torch.empty_like(rows), torch.empty_like(rows)
-            if stream is not None:
-                src.record_stream(stream)
-                dst.record_stream(stream)
+            src, dst = _b._outputs(stream, *(lambda: torch.empty_like(rows),) * 2)
             sp, dp = src.data_ptr(), dst.data_ptr()
         if copy_src is not None:
             src, sp = copy_src, self._given(copy_src, "copy_src", (n,))
