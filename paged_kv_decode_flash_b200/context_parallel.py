@@ -17,6 +17,8 @@ source (the CPU tests use the fp64 oracle over gloo).
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
+
 import numpy as np
 
 
@@ -85,11 +87,14 @@ class ContextParallelDecode:
     def __call__(self, dist, q, k_cache, v_cache, block_table, context_lens, key_begin,
                  key_count, *, causal, window, scale, kv_dtype, stream=None):
         """The full-context output, fp16 [B][nq][Hq][D], on every rank."""
+        import torch
         po, pl = self.partial(q, k_cache, v_cache, block_table, context_lens, key_begin,
                               key_count, causal=causal, window=window, scale=scale,
                               kv_dtype=kv_dtype, stream=stream)
         rows = po.numel() // po.shape[-1]
-        go, gl = exchange(po.reshape(rows, -1), pl.reshape(rows), dist)
+        # the gather takes the partials where they are made
+        with nullcontext() if stream is None else torch.cuda.stream(stream):
+            go, gl = exchange(po.reshape(rows, -1), pl.reshape(rows), dist)
         out, _ = self.B.merge(go, gl, stream=stream)
         return out.reshape(q.shape)
 

@@ -205,3 +205,25 @@ def test_attention_beside_a_busy_stream(lib, dt):
     got = beside_a_busy_stream(lambda s: B.merge(parts, lses, stream=s), want)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert dec.get_error() == 0 and plain.get_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# the context-parallel call: partial, gather and merge in one order
+# ---------------------------------------------------------------------------
+def test_the_gather_of_partials_runs_on_the_stream_that_makes_them(log, monkeypatch):
+    from paged_kv_decode_flash_b200 import context_parallel as CP
+    dec, args, i32 = decoder_on_the_host(B.PagedDecode)
+    cp = object.__new__(CP.ContextParallelDecode)
+    cp.B, cp.dec = B, dec
+    at = []
+
+    def exchange(po, pl, dist):
+        at.append(log.current)
+        return po[None], pl[None]
+
+    monkeypatch.setattr(CP, "exchange", exchange)
+    s = FakeStream()
+    kw = dict(causal=1, window=0, scale=0.1, kv_dtype=0)
+    cp(None, *args, i32(2), i32(2), stream=s, **kw)
+    cp(None, *args, i32(2), i32(2), **kw)
+    assert at == [s, "default"]
