@@ -234,8 +234,11 @@ class PagedDecode:
         self.workspace = workspace
         self.dims.workspace = _dptr(workspace)
         self.dims.workspace_bytes = workspace.numel() * workspace.element_size()
-        _check(lib().paged_attn_workspace_init(ctypes.byref(self.dims), _stream_ptr(None)),
-               "workspace_init")
+        _check(self._on(None, lambda st: lib().paged_attn_workspace_init(
+            ctypes.byref(self.dims), st)), "workspace_init")
+
+    def _on(self, stream, call):
+        return _on(self.workspace.device.index, stream, call)
 
     @classmethod
     def for_case(cls, case, device=None):
@@ -281,10 +284,10 @@ class PagedDecode:
         self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
         if out is None:
             out, = _outputs(stream, lambda: torch.empty_like(q))
-        rc = lib().paged_attn_decode(
+        rc = self._on(stream, lambda st: lib().paged_attn_decode(
             ctypes.byref(self.dims), _dptr(q), _dptr(k_cache), _dptr(v_cache),
             _dptr(block_table), _dptr(context_lens), self.n_query, int(causal), int(window),
-            float(scale), int(kv_dtype), _dptr(out), _stream_ptr(stream))
+            float(scale), int(kv_dtype), _dptr(out), st))
         _check(rc, "paged_attn_decode")
         return out
 
@@ -307,17 +310,18 @@ class PagedDecode:
                                                             device=q.device))
         _expect(out, "out", torch.float32, shp)
         _expect(out_lse, "out_lse", torch.float32, shp[:-1])
-        rc = lib().paged_attn_decode_partial(
+        rc = self._on(stream, lambda st: lib().paged_attn_decode_partial(
             ctypes.byref(self.dims), _dptr(q), _dptr(k_cache), _dptr(v_cache),
             _dptr(block_table), _dptr(context_lens), _dptr(key_begin), _dptr(key_count),
             self.n_query, int(causal), int(window), float(scale), int(kv_dtype), _dptr(out),
-            _dptr(out_lse), _stream_ptr(stream))
+            _dptr(out_lse), st))
         _check(rc, "paged_attn_decode_partial")
         return out, out_lse
 
     def get_error(self, stream=None) -> int:
         """Synchronises and returns (and clears) the device data-error status."""
-        return lib().paged_attn_get_error(ctypes.byref(self.dims), _stream_ptr(stream))
+        return self._on(stream,
+                        lambda st: lib().paged_attn_get_error(ctypes.byref(self.dims), st))
 
     def trace(self, q, k_cache, v_cache, block_table, context_lens, *, causal: int,
               window: int, scale: float, kv_dtype: int, out=None, stream=None):
@@ -329,10 +333,10 @@ class PagedDecode:
         B, nq, Hq = self.dims.num_seqs, self.n_query, self.dims.num_q_heads
         t, = _outputs(stream, lambda: torch.empty((B, nq, Hq, 5), dtype=torch.int32,
                                                   device=q.device))
-        rc = lib().paged_attn_trace(
+        rc = self._on(stream, lambda st: lib().paged_attn_trace(
             ctypes.byref(self.dims), _dptr(q), _dptr(k_cache), _dptr(v_cache),
             _dptr(block_table), _dptr(context_lens), nq, int(causal), int(window),
-            float(scale), int(kv_dtype), _dptr(out), _dptr(t), _stream_ptr(stream))
+            float(scale), int(kv_dtype), _dptr(out), _dptr(t), st))
         _check(rc, "paged_attn_trace")
         return out, t
 
@@ -350,10 +354,9 @@ class PagedDecode:
         cache = cache_shape(kv_dtype, d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
         _expect(k_cache, "k_cache", *cache)
         _expect(v_cache, "v_cache", *cache)
-        rc = lib().paged_attn_cache_write(
+        rc = self._on(stream, lambda st: lib().paged_attn_cache_write(
             ctypes.byref(d), _dptr(k_new), _dptr(v_new), _dptr(block_table),
-            _dptr(context_lens), self.n_query, int(kv_dtype), _dptr(k_cache), _dptr(v_cache),
-            _stream_ptr(stream))
+            _dptr(context_lens), self.n_query, int(kv_dtype), _dptr(k_cache), _dptr(v_cache), st))
         _check(rc, "paged_attn_cache_write")
 
 
@@ -374,8 +377,8 @@ def merge(partial_out: torch.Tensor, partial_lse: torch.Tensor, out=None, out_ls
     if out_lse is None:
         out_lse, = _outputs(stream, lambda: torch.empty((rows,), dtype=torch.float32,
                                                         device=partial_out.device))
-    rc = lib().paged_attn_merge(_dptr(partial_out), _dptr(partial_lse), S, rows, D,
-                                _dptr(out), _dptr(out_lse), _stream_ptr(stream))
+    rc = _on(partial_out.device.index, stream, lambda st: lib().paged_attn_merge(
+        _dptr(partial_out), _dptr(partial_lse), S, rows, D, _dptr(out), _dptr(out_lse), st))
     _check(rc, "paged_attn_merge")
     return out, out_lse
 
