@@ -228,7 +228,7 @@ class PagedDecode:
             raise PagedAttnError(PA_ERR_INVALID_ARG, "workspace_size (bad shapes)")
         self.workspace_bytes = int(need)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device or "cuda")
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda" if device is None else device)
         elif workspace.numel() * workspace.element_size() < need:
             raise PagedAttnError(PA_ERR_WORKSPACE, "workspace too small")
         self.workspace = workspace

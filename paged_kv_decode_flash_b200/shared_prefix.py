@@ -28,7 +28,7 @@ class SharedPrefixDecode(_b.PagedDecode):
         if need == 0:
             raise _b.PagedAttnError(_b.PA_ERR_INVALID_ARG, "shared_workspace_size (bad shapes)")
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device or "cuda")
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda" if device is None else device)
         elif workspace.numel() * workspace.element_size() < need:
             raise _b.PagedAttnError(_b.PA_ERR_WORKSPACE, "workspace too small")
         with torch.cuda.device(workspace.device):

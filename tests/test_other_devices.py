@@ -51,3 +51,30 @@ def test_calls_go_to_the_workspaces_device(asked, shared):
     for n, call in enumerate(calls):
         call()
         assert asked == [(dec.workspace.device.index, None)] * (n + 1)
+
+
+def made_on(monkeypatch, make):
+    """The devices that a constructor asks memory of."""
+    devices = []
+    empty = torch.empty
+
+    def logged(*a, **kw):
+        devices.append(kw.pop("device", None))
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", logged)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: __import__("contextlib").nullcontext())
+    make()
+    return devices
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("device,want", [(0, 0), (1, 1), (None, "cuda"), ("cuda:0", "cuda:0")])
+def test_device_0_is_a_device(asked, monkeypatch, shared, device, want):
+    """Whatever device is current; nothing is asked of "cuda" where one is named."""
+    from paged_kv_decode_flash_b200.shared_prefix import SharedPrefixDecode
+    dims = dict(num_seqs=2, num_q_heads=4, num_kv_heads=2, head_dim=128, block_size=16, max_blocks_per_seq=10,
+                num_blocks=25, n_query=1)
+    make = ((lambda: SharedPrefixDecode(prefix_blocks=7, device=device, **dims)) if shared else
+            (lambda: B.PagedDecode(device=device, **dims)))
+    assert made_on(monkeypatch, make) == [want]
