@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           if (phys < 0 || phys >= p.num_blocks) {
             misc[9] = 1;
             atomicOr(p.flags, kFlagBadBlock);
-            phys = 0;  // a stand-in: the rows that see it are marked
+            phys = -1;  // zeros are read: the rows that see it are marked, the others unharmed
           }
           return phys;
         };
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int key0 = base + t * kTileKeys + (2 * cw + h) * kChunk;
             const long long b = __shfl_sync(0xffffffffu, phys, h);
-            const bool on = t < te && key0 <= vhi;
+            const bool on = t < te && key0 <= vhi && b >= 0;
             const uint8_t* tile = cache + (b * p.num_kv_heads + g.kvh) * tile_bytes;
             const int slot = key0 % p.block_size;
             const uint8_t* at = tile + (slot + kq) * kHeadDim + cl * 16;
@@ -565,9 +565,11 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       auto row8_of = [&](int t, bool& bad) -> int {
         const int key0 = base + t * kTileKeys + lane * kChunk;
         if (lane >= kChunksPerTile || key0 > vhi) return -1;
-        int phys = __ldg(g.table + key0 / p.block_size);
+        const int phys = __ldg(g.table + key0 / p.block_size);
         bad = phys < 0 || phys >= p.num_blocks;
-        if (bad) phys = 0;  // a stand-in: the rows that see it are marked
+        // Rows behind the cache, which are read as zeros: the rows that see the
+        // block are marked, the others unharmed by what some other block holds.
+        if (bad) return (int)((long long)p.num_blocks * p.num_kv_heads * p.block_size / 8);
         return (int)((((long long)phys * p.num_kv_heads + g.kvh) * p.block_size + key0 % p.block_size) / 8);
       };
       auto issue = [&](bool isk, int T, int row8) {
