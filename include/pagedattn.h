@@ -303,7 +303,12 @@ int paged_attn_fork(const pa_dims* dims, int32_t* block_table, int32_t* context_
  * request) ask for the copy: the caller runs paged_attn_copy_blocks with
  * them on every layer's caches before it writes the new tokens.  When all
  * holders of a ragged page grow in one call, the last of them keeps it.
- * copy_src[i] = copy_dst[i] = -1 where nothing is to be copied.  Refused: a
+ * copy_src[i] = copy_dst[i] = -1 where nothing is to be copied.  A shorter
+ * length is carried out whatever the row's entries hold: one to be given up
+ * that is out of range (PA_ERR_BAD_BLOCK_INDEX), or whose page has a count of
+ * 0 already (PA_ERR_BAD_REQUEST), is passed over and reported, so that a row
+ * with damaged entries can be ended and the pages that it names are free
+ * again.  Refused: a
  * row out of range or named by an earlier request (PA_ERR_BAD_REQUEST), a
  * length outside [0, max_blocks_per_seq * block_size]
  * (PA_ERR_BAD_CONTEXT_LEN); from the first growing request on that the free
@@ -318,8 +323,10 @@ int paged_attn_resize(const pa_dims* dims, int32_t* block_table, int32_t* contex
  * to copy_src, copy_dst (device int32 [max(1, num_blocks / 2)], -1 behind
  * the last), their number to *count (device int32 [1]) and, for every page,
  * where it went to remap (device int32 [num_blocks], -1: free), for lists of
- * pages that the caller keeps elsewhere.  The caller runs
- * paged_attn_copy_blocks with the moves on every layer's caches. */
+ * pages that the caller keeps elsewhere.  An entry of a row that is out of
+ * range (PA_ERR_BAD_BLOCK_INDEX) or names a free page (PA_ERR_BAD_REQUEST) is
+ * left as it was and reported.  The caller runs paged_attn_copy_blocks with
+ * the moves on every layer's caches. */
 int paged_attn_compact(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
                        int32_t* ref_counts, int32_t* copy_src, int32_t* copy_dst, int32_t* count,
                        int32_t* remap, void* stream);

@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PageParam
         if (lane == 0) p.context_lens[row] = want;
       }
     } else if (stands) {
+      // (whatever the entries hold: a row with damaged ones can be ended)
       const int32_t* t = table_row(p, row);
       for (int b = pages_of(p, want) + lane; b < pages_of(p, L); b += 32) {
         const int pg = __ldcg(t + b);

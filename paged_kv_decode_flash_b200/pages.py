@@ -113,7 +113,8 @@ class PagePool:
         return src, dst
 
     def free(self, rows, *, stream=None) -> None:
-        """The rows end: length 0, their pages given up."""
+        """The rows end: length 0, their pages given up (of damaged entries
+        those that name a held page)."""
         self.resize(rows, stream=stream)
 
     def compact(self, *, stream=None) -> Moves:
