@@ -34,8 +34,9 @@
 //         high part and residual, K and V alike: S = Q K_hi + Q K_lo,
 //         O += P_hi V_hi + P_lo V_hi + P_hi V_lo (2^-22);
 //   int8 rows: qs enters as it is.  K's row scale multiplies the scores, V's
-//         the weights before their split, so that both cost no MMA; the
-//         row's reference covers the largest |V scale| of a tile, too.
+//         the weights before their split, so that both cost no MMA.  What has
+//         to fit fp16 is then weight x V scale: the reference of a row is the
+//         largest z_j + log2 |V scale j| (within 2^+-kScaleLog), key by key.
 // q8_0 runs single segments only: 128 rows leave shared memory for operands of
 // two tiles.
 //
@@ -103,6 +104,13 @@ constexpr int kStep = 64;       // keys of a step of a stream
 // heads' segments.)
 constexpr int kStart = 4;
 constexpr int kScaleSlots = 8;  // tiles whose row scales are kept: more than are in flight
+// int8 rows: a V scale counts as one between 2^-kScaleLog and 2^kScaleLog in a
+// row's reference.  Below, its products are nothing beside an fp16 output's
+// smallest step; above, an output is beyond fp16.  Two references whose weights
+// are within 2^30 of each other then differ by at most 2^126, and with the
+// weights up to kMaxWeight all sums stay inside fp32.
+constexpr int kScaleLog = 48;
+constexpr float kMaxWeight = 1.2676506e30f;  // 2^100
 
 constexpr int kSegSlots = 4;
 
@@ -141,8 +149,8 @@ struct Cfg {
   static constexpr uint32_t kBars = kV + VS * kSlot;
   static constexpr uint32_t kMisc = kBars + (BAR_COUNT * 8 + 15) / 16 * 16;         // int [16], see below
   static constexpr uint32_t kSegs = kMisc + 64;             // Segment [kSegSlots]
-  static constexpr uint32_t kScales = kSegs + kSegSlots * 64;  // int8 rows: float K [8][128], V [8][128], max [8][4]
-  static constexpr uint32_t kTotal = kScales + (kRow ? kScaleSlots * (2 * 128 + 4) * 4 : 0);
+  static constexpr uint32_t kScales = kSegs + kSegSlots * 64;  // int8 rows: float K [8][128], V, log2 |V|
+  static constexpr uint32_t kTotal = kScales + (kRow ? kScaleSlots * 3 * 128 * 4 : 0);
   static_assert(kBars % 16 == 0 && kSegs % 16 == 0 && kScales % 16 == 0, "alignment");
   static_assert(kTotal + 1024 <= 232448, "shared memory per CTA");
 };
@@ -439,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
       const int full = isk ? BAR_KFULL : BAR_VFULL, empty = isk ? BAR_KEMPTY : BAR_VEMPTY;
       const uint8_t* cache = static_cast<const uint8_t*>(isk ? p.k : p.v);
       const long long tile_bytes = quant_tile_bytes(KV, p.block_size);
-      float* scales = reinterpret_cast<float*>(smem + C::kScales);  // K [8][128], V, max [8][4]
+      float* scales = reinterpret_cast<float*>(smem + C::kScales);  // K [8][128], V, log2 |V|
       int T = 0, st = 0, ph = 0;
       bool ok = true;
       segments([&](const Segment& g) {
@@ -499,11 +507,10 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               scales[ss * 128 + 32 * cw + lane] = d1 * cs;
             } else {  // scales of hidden keys may be anything
               const float d = kw + lane >= vlo && kw + lane <= vhi ? d1 : 0.f;
-              float mx = fabsf(d);
+              const int ex = (int)(__float_as_uint(fabsf(d)) >> 23) - 126;  // |d| < 2^ex
               scales[(kScaleSlots + ss) * 128 + 32 * cw + lane] = d;
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              if (lane == 0) scales[2 * kScaleSlots * 128 + ss * 4 + cw] = mx;
+              scales[(2 * kScaleSlots + ss) * 128 + 32 * cw + lane] =
+                  (float)min(max(ex, -kScaleLog), kScaleLog);
             }
           }
           const bool inside = isk || (kw >= vlo && kw + 31 <= vhi);
@@ -908,10 +915,11 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           fence_proxy_async_smem();
         }
         if (warp_rows) {
-          // int8 rows: the tile's scales of K (times the softmax scale) and V.
+          // int8 rows: the tile's scales of K (times the softmax scale), V, log2 |V|.
           const float4* ks = reinterpret_cast<const float4*>(smem + C::kScales) + T % kScaleSlots * 32 +
                              half * (kStep / 4);
           const float4* vs = ks + kScaleSlots * 32;
+          const float4* vlog = vs + kScaleSlots * 32;
           // Hidden keys among the 32 from kb + 32 c: -inf in their place.
           auto mask = [&](float (&v)[32], int c) {
             if (whole) return;
@@ -922,18 +930,10 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (!(see >> i & 1)) v[i] = -INFINITY;
           };
-          // int8 rows: the scores times K's row scales, and the power of two
-          // above the step's largest |V scale|.
-          float vtop = 0.f;
-          if constexpr (kRow) {
+          if constexpr (kRow) {  // the V scales are there
             const int st = T % C::VS;
             ok = __all_sync(0xffffffffu, wait(BAR_VFULL + st, T / C::VS));
             if (!ok) break;
-            const float2 q2 = *(reinterpret_cast<const float2*>(smem + C::kScales) +
-                                4 * kScaleSlots * 32 + T % kScaleSlots * 2 + half);
-            const float vm = fmaxf(q2.x, q2.y);
-            const int ex = (int)(__float_as_uint(vm) >> 23) - 126;  // vm < 2^ex
-            vtop = (float)min(max(ex, -64), 64);
           }
           auto scaled = [&](float (&v)[32], int c) {
             if constexpr (kRow) {
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           // Scores to weights, in place; their sum.
           float2 sum, sum2;
           auto weights = [&](float (&v)[32]) {
-            const float k = kRow ? 1.f : cs;  // (int8 rows: scaled already)
+            const float k = cs;
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 z = fma2(make_float2(v[e], v[e + 1]), make_float2(k, k), make_float2(bias, bias));
@@ -960,10 +960,10 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               to = add2(to, make_float2(v[e], v[e + 1]));
             }
           };
-          // Moves the reference of the rows that `need` it to `top`, and what the
-          // stream has accumulated for them.
+          // Moves the reference of the rows that `need` it up to `top`, and what
+          // the stream has accumulated for them.
           auto move = [&](bool need, float top) -> bool {
-            const float mn = need && top != -INFINITY ? top : m;
+            const float mn = need ? fmaxf(m, top) : m;
             const bool moved = mn != m;
             const float f = moved ? fast_exp2(m - mn) : 1.f;
             m = mn;
@@ -995,8 +995,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           auto pack = [&](const float (&v)[32], int c, int z) {  // from key 2 z of the chunk on
 #pragma unroll
             for (int i = 0; i < kPack; ++i) {
-              float2 x = make_float2(v[2 * (z + i)], v[2 * (z + i) + 1]);
-              if constexpr (kRow) x = mul2(x, reinterpret_cast<const float2*>(vs)[c * 16 + z + i]);
+              const float2 x = make_float2(v[2 * (z + i)], v[2 * (z + i) + 1]);
               ph[i] = h2_bits(__floats2half2_rn(x.x, x.y));
               const float2 lo2 = residual(x, ph[i]);
               pl[i] = h2_bits(__floats2half2_rn(lo2.x, lo2.y));
@@ -1009,17 +1008,26 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
           if constexpr (!kHold) {
             // 32 columns at a time: the converters leave no registers for a
             // step's 64 scores.  As below, a row keeps its reference while its
-            // sums stay below the limit.
-            auto top_of = [&](int x) -> float {  // the chunk's maximum, read again
+            // sums stay below the limit: of the weights, or, int8 rows, of the
+            // squares of what is rounded to fp16, so that the V scale of a key
+            // with little weight costs the others nothing.
+            auto top_of = [&](int x) -> float {  // the chunk's largest, read again
               tmem_ld32(tS + x * 32, va);
               tmem_ld_wait(va);
               scaled(va, x);
               float mx = -INFINITY;  // (scores of NaN are passed over)
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) mx = max3(mx, va[e], va[e + 1]);
-              return (kRow ? mx : mx * cs) + vtop;
+              for (int e = 0; e < 32; e += 4) {
+                if constexpr (kRow) {
+                  const float4 g = vlog[x * 8 + e / 4];
+                  va[e] += g.x; va[e + 1] += g.y; va[e + 2] += g.z; va[e + 3] += g.w;
+                }
+                mx = max3(mx, va[e], va[e + 1]);
+                mx = max3(mx, va[e + 2], va[e + 3]);
+              }
+              return kRow ? mx : mx * cs;
             };
-            auto chunk_weights = [&](int x) -> float {
+            auto chunk_weights = [&](int x, bool& fits) -> float {
               tmem_ld32(tS + x * 32, va);
               tmem_ld_wait(va);
 #pragma unroll
@@ -1031,27 +1039,39 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
                 va[e] = a.x; va[e + 1] = a.y; va[e + 2] = b.x; va[e + 3] = b.y;
               }
               mask(va, x);
-              float2 a = make_float2(0.f, 0.f), b = a;
+              float2 a = make_float2(0.f, 0.f), b = a, sq = a;
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) va[e + i] = fast_exp2(va[e + i]);
-                a = add2(a, make_float2(va[e], va[e + 1]));
-                b = add2(b, make_float2(va[e + 2], va[e + 3]));
+                float2 u = make_float2(va[e], va[e + 1]), w = make_float2(va[e + 2], va[e + 3]);
+                a = add2(a, u);
+                b = add2(b, w);
+                if constexpr (kRow) {
+                  const float4 g = vs[x * 8 + e / 4];
+                  u = mul2(u, make_float2(g.x, g.y));
+                  w = mul2(w, make_float2(g.z, g.w));
+                  sq = fma2(u, u, sq);
+                  sq = fma2(w, w, sq);
+                  va[e] = u.x; va[e + 1] = u.y; va[e + 2] = w.x; va[e + 3] = w.y;
+                }
               }
-              return (a.x + a.y) + (b.x + b.y);
+              const float total = (a.x + a.y) + (b.x + b.y);
+              fits = kRow ? sq.x + sq.y <= kSumLimit * kSumLimit && total <= kMaxWeight
+                          : total <= kSumLimit;
+              return total;
             };
             if (fresh) {  // rows at their first keys
               const float t0 = top_of(0), top = fmaxf(t0, top_of(1));
               if (!move(mine && m == -INFINITY, top)) break;
               fresh = __any_sync(0xffffffffu, mine && m == -INFINITY);
             }
-            const float most = kRow ? fast_exp2(-vtop) * kSumLimit : kSumLimit;
             bool up = true;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float total = chunk_weights(x);
-              const bool need = mine && m != -INFINITY && !(total <= most);
+              bool fits;
+              float total = chunk_weights(x, fits);
+              const bool need = mine && m != -INFINITY && !fits;
               if (__any_sync(0xffffffffu, need)) {
                 const float before = m;
                 up = move(need, top_of(x));
@@ -1075,7 +1095,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
                   tmem_st<16>(tS, va);
                   tmem_st<16, 16>(tS + 16, va);
                 }
-                total = chunk_weights(x);
+                total = chunk_weights(x, fits);
               }
               l += total;
 #pragma unroll
@@ -1096,15 +1116,13 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
             };
             tmem_ld_wait(va);
             tmem_ld_wait(vb);
-            // The weights against the reference so far; a row whose sum (times
-            // the largest |V scale|) stays below the limit keeps it, without its
-            // maximum ever being taken.
+            // The weights against the reference so far; a row whose sum stays
+            // below the limit keeps it, without its maximum ever being taken.
             float total = 0.f;
             bool need = mine;
             if (y > 0) {
               total = all_weights();
-              const float most = kRow ? total * fast_exp2(vtop) : total;
-              need = mine && (m == -INFINITY || !(most <= kSumLimit));
+              need = mine && (m == -INFINITY || !(total <= kSumLimit));
               pack(va, 0, 0);  // (in the shadow of the vote)
             }
             if (__any_sync(0xffffffffu, need)) {
@@ -1121,8 +1139,7 @@ __global__ void __launch_bounds__(Cfg<KV>::kThreads, 1)
               float mx = -INFINITY;
 #pragma unroll
               for (int e = 0; e < 32; ++e) mx = max3(mx, va[e], vb[e]);
-              const float top = (kRow ? mx : mx * cs) + vtop;
-              if (!move(need, top)) break;
+              if (!move(need, mx * cs)) break;
               sum = sum2 = make_float2(0.f, 0.f);
               weights(va);
               weights(vb);
