@@ -289,7 +289,8 @@ int paged_attn_pages_workspace_init(const pa_dims* dims, void* stream);
  * holds the same pages, the ragged last one included (device int32 [n],
  * n <= num_seqs).  No data moves.  Refused (PA_ERR_BAD_REQUEST): a row out
  * of range, a child that is not empty or that an earlier request has, a
- * parent that is a child of the same call. */
+ * parent that is a child of the same call.  The requests are compared with
+ * each other: meant for up to some thousands a call. */
 int paged_attn_fork(const pa_dims* dims, int32_t* block_table, int32_t* context_lens,
                     int32_t* ref_counts, const int32_t* parents, const int32_t* children,
                     int32_t n, void* stream);
