@@ -145,6 +145,14 @@ def _outputs(stream, *makes):
     return made
 
 
+def _like(t, stream):
+    """torch.empty_like(t) for work on `stream` (short calls are host time: no
+    closure where there is no stream)."""
+    if stream is None:
+        return torch.empty_like(t)
+    return _outputs(stream, lambda: torch.empty_like(t))[0]
+
+
 def _on(index: int, stream, call):
     """call(stream pointer) with device `index` current; stream None: its
     current one."""
@@ -283,7 +291,7 @@ class PagedDecode:
                  window: int, scale: float, kv_dtype: int, out=None, stream=None):
         self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
         if out is None:
-            out, = _outputs(stream, lambda: torch.empty_like(q))
+            out = _like(q, stream)
         rc = self._on(stream, lambda st: lib().paged_attn_decode(
             ctypes.byref(self.dims), _dptr(q), _dptr(k_cache), _dptr(v_cache),
             _dptr(block_table), _dptr(context_lens), self.n_query, int(causal), int(window),
@@ -329,7 +337,7 @@ class PagedDecode:
         kernel that read the cache.  Returns (out, trace int32 [B][nq][Hq][5])."""
         self.check_args(q, k_cache, v_cache, block_table, context_lens, kv_dtype, out)
         if out is None:
-            out, = _outputs(stream, lambda: torch.empty_like(q))
+            out = _like(q, stream)
         B, nq, Hq = self.dims.num_seqs, self.n_query, self.dims.num_q_heads
         t, = _outputs(stream, lambda: torch.empty((B, nq, Hq, 5), dtype=torch.int32,
                                                   device=q.device))

@@ -102,7 +102,7 @@ class PagePool:
         rp = self._given(rows, "rows", (n,))
         lp = None if new_lens is None else self._given(new_lens, "new_lens", (n,))
         if copy_src is None or copy_dst is None:
-            src, dst = _b._outputs(stream, *(lambda: torch.empty_like(rows),) * 2)
+            src, dst = _b._like(rows, stream), _b._like(rows, stream)
             sp, dp = src.data_ptr(), dst.data_ptr()
         if copy_src is not None:
             src, sp = copy_src, self._given(copy_src, "copy_src", (n,))

@@ -79,7 +79,7 @@ class SharedPrefixDecode(_b.PagedDecode):
                 _b._given(context_lens, "context_lens", torch.int32, (d.num_seqs,), dev),
                 *self.check_shared(prefix_table, prefix_len))
         if out is None:
-            out, = _b._outputs(stream, lambda: torch.empty_like(q))
+            out = _b._like(q, stream)
         op = _b._given(out, "out", torch.float16, qshape, dev)
         _b._check(_b._on(dev.index, stream, lambda st: _b.lib().paged_attn_decode_shared(
             d, *args, self.prefix_blocks, self.n_query, int(causal), int(window), float(scale),
