@@ -187,7 +187,9 @@ int paged_attn_decode_partial(const pa_dims* dims, const void* q, const void* k_
  * that some row sees, may reach every row); a row with a score of NaN or
  * +infinity is NaN.  The workspace must have
  * paged_attn_shared_workspace_size bytes, be initialised by
- * paged_attn_workspace_init and may serve paged_attn_decode calls too. */
+ * paged_attn_workspace_init and may serve paged_attn_decode calls too (of the
+ * same num_seqs and num_kv_heads: the counters of others may lie where this
+ * call's partials do). */
 int paged_attn_decode_shared(const pa_dims* dims, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* block_table,
                              const int32_t* context_lens, const int32_t* prefix_table,

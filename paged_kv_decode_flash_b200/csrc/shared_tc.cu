@@ -40,6 +40,12 @@
 // q8_0 runs single segments only: 128 rows leave shared memory for operands of
 // two tiles.
 //
+// Precision.  The tensor cores add to O in 32 bits but cut off what does not
+// fit, toward zero, twice for every 16 keys (P_hi V, P_lo V).  Over a CTA's run
+// of keys that is a bias: 2e-5 of the output's size after 14,000 keys, 8.5e-5
+// after 113,000 (fp16's half step: 4.9e-4).  The sums of weights, the join and
+// all references are rounded to nearest.
+//
 // Roles: warps 0-7 the softmax, which also stages Q and writes the partials.
 // Then, fp16: a producer (TMA boxes of 16 keys through the block table);
 // int8: eight converters (raw bytes through registers, one tile ahead).  Then
@@ -50,7 +56,8 @@
 // Bounds.  Many rows: the tensor cores.  A step's products take 8 x 49 cycles
 // (Q K^T with N = 64: Q and K come from shared memory, 6 KB a product) and
 // 8 x 64 (P V), 1808 for both streams; a pair of steps was measured at 2210
-// (512 rows a KV head, 8 of them, 131072 keys: 392 us), 2366 with the commits
+// (512 rows a KV head, 8 of them, 131072 keys: 392 us at full clocks, 463 to 475
+// in a row of such calls under the power cap), 2366 with the commits
 // between the products and V awaited behind P, 4800 with one issuer that is one
 // lane.  The exponentials (2 x 64 a lane, 1024 cycles) and the conversions
 // to fp16 share what is left.  q8_0: 4400 a pair, int8 rows 3440, set by the
