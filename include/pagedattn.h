@@ -183,9 +183,10 @@ int paged_attn_decode_partial(const pa_dims* dims, const void* q, const void* k_
  * PA_ERR_BAD_BLOCK_INDEX.  Results need not be bit-identical to
  * paged_attn_decode's (another order of the sums); repeated calls give
  * bit-identical results, and a sequence's result does not depend on the
- * finite values of the others (a value that is not finite, in a prefix key
- * that some row sees, may reach every row); a row with a score of NaN or
- * +infinity is NaN.  The workspace must have
+ * finite values of the others (a value that is not finite may reach every
+ * row where it is in a prefix key that some row sees, and every row of its
+ * sequence where it is in a key of its own that some row sees); a row with a
+ * score of NaN or +infinity is NaN.  The workspace must have
  * paged_attn_shared_workspace_size bytes, be initialised by
  * paged_attn_workspace_init and may serve paged_attn_decode calls too (of the
  * same num_seqs and num_kv_heads: the counters of others may lie where this
