@@ -163,6 +163,7 @@ struct Misc {
   int nqk, npv;                // QK and PV products issued (drains)
   int k_conv, v_conv;          // int8: tiles converted (drains)
   int n_merge;                 // mode 1: groups this CTA merges at the end
+  int merge_more;              // ... 1 + the first of those that its list has no room for, 0: none
   int own_group;               // mode 0: the KV head whose merge this CTA shares (-1: none)
   int own_phase;               // ... its barrier phase before this call's arrivals
   int own_first, own_count;    // ... its partials: CTAs [first, first + count) of the set
@@ -419,6 +420,17 @@ __device__ __forceinline__ bool arrive(const DecodeParams& p, int group, int exp
   return false;
 }
 
+// Mode 1: notes a completed group that this CTA merges at the end.  A batch of
+// many groups may complete more of them in one CTA than its list holds: the
+// others are chained through their mode 0 counters, which mode 1 does not use
+// and which are 0 again when they have been merged.
+__device__ __forceinline__ void list_merge(const DecodeParams& p, int& n_merge, int& more, int* list,
+                                           int group) {
+  const int k = atomicAdd(&n_merge, 1);
+  if (k < kMergeListLen) list[k] = group;
+  else atomicExch(group_counter(p, group), atomicExch(&more, group + 1));
+}
+
 // ------------------------------------------------------------------ merges
 // Merge of S consecutive partial slots [slot0, slot0 + S) of one group into
 // its output rows, the (row, float4 column) pairs [pa, pb) of it: M = max_k
@@ -612,6 +624,7 @@ __global__ void __launch_bounds__(Cfg<RW, NG, KV>::kThreads, 1)
       misc->abort = 0;
       misc->nqk = misc->npv = misc->k_conv = misc->v_conv = 0;
       misc->n_merge = 0;
+      misc->merge_more = 0;
       misc->own_group = -1;
       misc->segs_published = 0;
       misc->segs_done[0] = misc->segs_done[1] = 0;
@@ -1425,8 +1438,7 @@ __global__ void __launch_bounds__(Cfg<RW, NG, KV>::kThreads, 1)
           for (int i = 0; i < npend; ++i) {
             const int* pe = pend + i * 3;
             if (arrive(p, pe[0], pe[1], pe[2] != 0, 1)) {
-              const int k = atomicAdd(&misc->n_merge, 1);  // complete: merge it at the end
-              if (k < kMergeListLen) merge_list[k] = pe[0];
+              list_merge(p, misc->n_merge, misc->merge_more, merge_list, pe[0]);
             }
           }
           misc->segs_done[g] = pend_last + 1;
@@ -1823,8 +1835,7 @@ __global__ void __launch_bounds__(Cfg<RW, NG, KV>::kThreads, 1)
           p.part_lse[(long long)si.slot * p.rows_half + r] = __uint_as_float(kInvalidLse);
         __threadfence();
         if (arrive(p, si.group, si.expect, si.first && g == 0, 1)) {
-          const int i = atomicAdd(&misc->n_merge, 1);
-          if (i < kMergeListLen) merge_list[i] = si.group;
+          list_merge(p, misc->n_merge, misc->merge_more, merge_list, si.group);
         }
       }
     }
@@ -1863,8 +1874,17 @@ __global__ void __launch_bounds__(Cfg<RW, NG, KV>::kThreads, 1)
     // Groups this CTA completed: merge each, whole.
     const int n = min(misc->n_merge, kMergeListLen);
     if (n > 0) __threadfence();  // the other CTAs' partials, published before their counts
-    for (int i = 0; i < n; ++i) {
-      const int grp = merge_list[i];
+    int next = misc->merge_more;
+    for (int i = 0; i < n || next != 0; ++i) {
+      int grp;
+      if (i < n) {
+        grp = merge_list[i];
+      } else {
+        grp = next - 1;
+        next = __ldcg(group_counter(p, grp));
+        __syncthreads();  // read by all
+        if (threadIdx.x == 0) *group_counter(p, grp) = 0;
+      }
       const int h = grp % H, kvh = (grp / H) % Hkv, s = grp / (H * Hkv);
       const int L = ld_nc_s32(p.context_lens + s);
       int nb, ns;
