@@ -23,6 +23,11 @@ namespace {
 constexpr int kMaxSmsAnyDevice = 4096;  // bound used to size workspaces without a device
 constexpr int kMaxItemTiles = 16;       // mode 1: tiles per big item
 constexpr int kMaxSubItems = 4;         // mode 1: the last item of a group is cut into up to 4
+// Mode 1: big items of a group, at most.  A CTA merges a group's partials
+// through some 200 KB of shared memory, 20 bytes a partial: tables of more than
+// 8.4 million keys get larger items (at 20.9 million, items of kMaxItemTiles
+// would have overrun it).
+constexpr int kMaxGroupItems = 4096;
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -116,7 +121,8 @@ Plan make_plan(const pa_dims* d, int n_query, int kv_dtype, int sms) {
     // A batch: items of T tiles (the last one of a group in up to four
     // pieces) from a queue, one CTA per SM; one launch per kMaxQueueSeqs
     // sequences.
-    const long long T = std::min<long long>(kMaxItemTiles, max_tiles);
+    const long long T = std::max<long long>(std::min<long long>(kMaxItemTiles, max_tiles),
+                                            ceil_div(max_tiles, kMaxGroupItems));
     pl.mode = 1;
     pl.item_tiles = (int)T;
     pl.slots_per_group = (int)(ceil_div(max_chunks(d), 8 * T) - 1 + kMaxSubItems);
